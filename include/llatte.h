@@ -443,6 +443,160 @@ int llatte_tokenizer_uses_tensor_cores(const llatte_tokenizer* tok);
 /* Free the tokenizer (synchronises its device); the tables stay the caller's. */
 void llatte_tokenizer_destroy(llatte_tokenizer* tok);
 
+/*
+ * Paged latent cache: the latent K = V rows of users' histories kept between
+ * requests, so that a request computes only its new events.  The pages have
+ * no counterpart of it (they describe one batch at a time); the attention is
+ * the absorbed form of appendix A.3 with the visibility rules of
+ * llatte_forward, over rows that lie in pages.
+ *
+ * Layout.  A pool of n_pages pages of page_size rows of `rank` elements.
+ * User u's event t (0 = earliest) lies in row t % page_size of page
+ * table[u * table_stride + t / page_size].  An optional second pool holds one
+ * fp32 number per row, the attention weight the event has collected (its
+ * "mass"); it shares the page table.  Both pools are the caller's device
+ * memory and are referenced, not copied; the caller also hands out pages.
+ *
+ *   heads, rank     query heads h and latent rank r; r * element size a
+ *                   multiple of 16 bytes, r <= 256
+ *   dtype           LLATTE_BF16 or LLATTE_FP32, of pool, queries and outputs
+ *                   (sums, softmax statistics and masses are fp32); bf16 with
+ *                   r = 64, 128 or 256 runs on the tensor cores
+ *   page_size       16, 32, 64 or 128
+ *   n_pages         pages of the pool, n_pages * page_size < 2^31
+ *   max_batch       most users of one call (<= LLATTE_CACHE_MAX_BATCH)
+ *   max_pages       most pages one user may hold
+ *   max_rows        most query rows of one call, max_rows * heads < 2^31
+ *
+ * Faults that only the device can see set bits in the cache's status word: a
+ * user whose offsets decrease, are negative or pass the rows given, or who has
+ * more new rows than cached events (LLATTE_DEV_BAD_OFFSETS), or whose length is
+ * negative or above its pages (LLATTE_DEV_TOO_LONG), is left out of the call;
+ * a page id outside the pool (LLATTE_DEV_BAD_ID) reads as zero rows and is
+ * never written.
+ *
+ * Calls on one cache share its workspace: they must not overlap in time, and
+ * neither may two replays of graphs captured from them.
+ */
+#define LLATTE_CACHE_MAX_BATCH 4096
+typedef struct {
+  int32_t heads, rank, dtype, page_size;
+  int32_t n_pages, max_batch, max_pages;
+  int64_t max_rows;
+} llatte_cache_dims;
+
+typedef struct llatte_cache llatte_cache;
+
+/* Bytes of device workspace a cache with these dims allocates (0 on bad dims). */
+size_t llatte_cache_workspace_bytes(const llatte_cache_dims* dims);
+
+/*
+ * Create a cache on the current device (synchronous).  pool: device
+ * [n_pages, page_size, rank] in dtype, 16-byte aligned; mass: device fp32
+ * [n_pages, page_size], or NULL when no call accumulates or evicts.
+ */
+int llatte_cache_create(llatte_cache** cache, const llatte_cache_dims* dims, void* pool,
+                        float* mass);
+
+/*
+ * The users of one call.
+ *   table         device int32 [B, table_stride], the page ids of every user
+ *   lengths       device int32 [B], cached events, the call's new ones included
+ */
+typedef struct {
+  const int32_t* table;
+  int32_t table_stride;
+  const int32_t* lengths;
+  int32_t B;
+} llatte_cache_view;
+
+/*
+ * Append: user u's rows x[offsets[u]] .. x[offsets[u+1] - 1] become its newest
+ * events, slots lengths[u] - m .. lengths[u] - 1.  With gain != NULL each row is
+ * first normalised, c = x / sqrt(mean(x^2) + eps) * gain (fp32 statistics, one
+ * rounding to dtype).  The appended rows' masses are set to 0.
+ *   x        device [rows, rank] in dtype, 16-byte aligned
+ *   offsets  device int64 [B+1], non-decreasing, offsets[B] <= rows
+ *   gain     device [rank] in dtype, 16-byte aligned, or NULL
+ * Asynchronous on `stream`.  Appending the same rows again changes nothing.
+ */
+int llatte_cache_append(llatte_cache* cache, const llatte_cache_view* view, const void* x,
+                        int64_t rows, const int64_t* offsets, const void* gain, float eps,
+                        void* stream);
+
+/*
+ * Attention of new rows over the cache.  User u's query rows are
+ * q_offsets[u] .. q_offsets[u+1] - 1: first its m newest events (already
+ * appended), then its last n_cand rows (or all, if it has fewer), the query
+ * tokens.  With p the position of a new event, and p = lengths[u] - 1 for a
+ * query token, a row sees event t when
+ *     t <= p  and  (window == 0  or  t > p - window  or  t < n_sink),
+ * and every head gives
+ *     out = sum_t softmax_t(scale * q . c_t) c_t,   lse = log sum_t exp(scale * q . c_t).
+ * A row that sees nothing gives out = 0 and lse = -infinity.  What a row does
+ * not see has no effect on it, whatever its bits; a row that sees a latent with
+ * an infinity or NaN gives no finite result.
+ *   q, out       device [rows, heads, rank] in dtype, 16-byte aligned; rows of
+ *                `out` that belong to no user are left as they were
+ *   lse          device fp32 [rows, heads], or NULL
+ *   window       events a row sees back from its position, itself included
+ *                (0 = all);  n_sink: first events that stay visible
+ *   accumulate   1: the weights of all rows and heads are added to the masses of
+ *                the events they fall on (fp32, in a fixed order)
+ * Asynchronous on `stream`.
+ */
+typedef struct {
+  const void* q;
+  const int64_t* q_offsets;
+  int64_t rows;
+  int32_t n_cand;
+  float scale;
+  int32_t window, n_sink;
+  void* out;
+  float* lse;
+  int32_t accumulate;
+} llatte_cache_attn;
+int llatte_cache_attend(llatte_cache* cache, const llatte_cache_view* view,
+                        const llatte_cache_attn* args, void* stream);
+
+/*
+ * Eviction by accumulated attention weight.  A user with T > budget events
+ * keeps its first n_sink, its last n_recent and, of the others, the
+ * budget - n_sink - n_recent with the largest masses (equal masses: the
+ * earlier event; NaN counts as the smallest); a user with T <= budget keeps
+ * all.  The kept events and their masses are packed in order into the pages of
+ * dst_table, or into the user's own first pages (dst_table == NULL), whose
+ * other rows stay as they were.
+ *   budget        >= 1;  n_sink + n_recent <= budget
+ *   dst_table     device int32 [B, dst_stride] of pages that no other row of
+ *                 either table names, or NULL
+ *   new_lengths   device int32 [B], may be the view's lengths
+ *   kept          device int32 [B, budget] or NULL: the old slots of the kept
+ *                 events, ascending; entries past the new length are left as
+ *                 they were
+ * No page may belong to two users here.  Needs the mass pool
+ * (LLATTE_ERR_ARG).  Asynchronous on `stream`.
+ */
+typedef struct {
+  int32_t budget, n_sink, n_recent;
+  const int32_t* dst_table;
+  int32_t dst_stride;
+  int32_t* new_lengths;
+  int32_t* kept;
+} llatte_cache_evict_args;
+int llatte_cache_evict(llatte_cache* cache, const llatte_cache_view* view,
+                       const llatte_cache_evict_args* args, void* stream);
+
+/* Synchronise the device, read the status word and clear it (as
+ * llatte_get_status does for a forward handle). */
+int llatte_cache_get_status(llatte_cache* cache, int32_t* device_status);
+
+/* 1 when attention over the cache runs on the tensor cores, 0 on CUDA cores. */
+int llatte_cache_uses_tensor_cores(const llatte_cache* cache);
+
+/* Free the cache's workspace (synchronises its device); the pools stay the caller's. */
+void llatte_cache_destroy(llatte_cache* cache);
+
 /* Free the handle and everything it owns (synchronises its device). */
 void llatte_destroy(llatte_handle* handle);
 

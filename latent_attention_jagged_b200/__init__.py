@@ -7,6 +7,7 @@ opened when a handle is created, and a missing library is an error.
 from . import cost
 
 __all__ = ["cost"]
-from .binding import Llatte, LlatteError, Tokenizer, load_library  # noqa: E402  (no library load here)
+from .binding import (  # noqa: E402  (no library load here)
+    LatentCache, Llatte, LlatteError, Tokenizer, load_library)
 
-__all__ += ["Llatte", "LlatteError", "Tokenizer", "load_library"]
+__all__ += ["LatentCache", "Llatte", "LlatteError", "Tokenizer", "load_library"]

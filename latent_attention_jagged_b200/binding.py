@@ -80,13 +80,42 @@ class llatte_attn_export(ctypes.Structure):
                 ("topk", ctypes.c_void_p), ("hours", ctypes.c_void_p)]
 
 
+class llatte_cache_dims(ctypes.Structure):
+    _fields_ = [("heads", ctypes.c_int32), ("rank", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("max_batch", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("max_rows", ctypes.c_int64)]
+
+
+class llatte_cache_view(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("table_stride", ctypes.c_int32),
+                ("lengths", ctypes.c_void_p), ("B", ctypes.c_int32)]
+
+
+class llatte_cache_attn(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("q_offsets", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("n_cand", ctypes.c_int32), ("scale", ctypes.c_float), ("window", ctypes.c_int32),
+                ("n_sink", ctypes.c_int32), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("accumulate", ctypes.c_int32)]
+
+
+class llatte_cache_evict_args(ctypes.Structure):
+    _fields_ = [("budget", ctypes.c_int32), ("n_sink", ctypes.c_int32),
+                ("n_recent", ctypes.c_int32), ("dst_table", ctypes.c_void_p),
+                ("dst_stride", ctypes.c_int32), ("new_lengths", ctypes.c_void_p),
+                ("kept", ctypes.c_void_p)]
+
+
 EXPORTS = ("llatte_create", "llatte_forward", "llatte_plan_export", "llatte_get_status",
            "llatte_workspace_bytes", "llatte_error_string", "llatte_destroy",
            "llatte_set_profiling", "llatte_profile_reset", "llatte_profile_step",
            "llatte_plan_static", "llatte_exp2_eval", "llatte_forward_export",
            "llatte_forward_batch", "llatte_attn_form_mask", "llatte_tokenizer_create",
            "llatte_tokenize", "llatte_tokenizer_get_status", "llatte_tokenizer_uses_tensor_cores",
-           "llatte_tokenizer_destroy", "llatte_inject_timeout")
+           "llatte_tokenizer_destroy", "llatte_inject_timeout", "llatte_cache_workspace_bytes",
+           "llatte_cache_create", "llatte_cache_append", "llatte_cache_attend",
+           "llatte_cache_evict", "llatte_cache_get_status", "llatte_cache_uses_tensor_cores",
+           "llatte_cache_destroy")
 TOK_MAX_FIELDS = 8
 PLAN_STATIC_MAX_BATCH = 4096
 
@@ -149,6 +178,23 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.llatte_tokenizer_uses_tensor_cores.restype = ctypes.c_int
     lib.llatte_tokenizer_destroy.argtypes = [VP]
     lib.llatte_tokenizer_destroy.restype = None
+    lib.llatte_cache_workspace_bytes.argtypes = [P(llatte_cache_dims)]
+    lib.llatte_cache_workspace_bytes.restype = ctypes.c_size_t
+    lib.llatte_cache_create.argtypes = [P(VP), P(llatte_cache_dims), VP, VP]
+    lib.llatte_cache_create.restype = ctypes.c_int
+    lib.llatte_cache_append.argtypes = [VP, P(llatte_cache_view), VP, I64, VP, VP,
+                                        ctypes.c_float, VP]
+    lib.llatte_cache_append.restype = ctypes.c_int
+    lib.llatte_cache_attend.argtypes = [VP, P(llatte_cache_view), P(llatte_cache_attn), VP]
+    lib.llatte_cache_attend.restype = ctypes.c_int
+    lib.llatte_cache_evict.argtypes = [VP, P(llatte_cache_view), P(llatte_cache_evict_args), VP]
+    lib.llatte_cache_evict.restype = ctypes.c_int
+    lib.llatte_cache_get_status.argtypes = [VP, P(I32)]
+    lib.llatte_cache_get_status.restype = ctypes.c_int
+    lib.llatte_cache_uses_tensor_cores.argtypes = [VP]
+    lib.llatte_cache_uses_tensor_cores.restype = ctypes.c_int
+    lib.llatte_cache_destroy.argtypes = [VP]
+    lib.llatte_cache_destroy.restype = None
     if path is None:
         _lib = lib
     return lib
@@ -513,6 +559,169 @@ class Tokenizer:
     def close(self):
         if getattr(self, "h", None):
             self.lib.llatte_tokenizer_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class LatentCache:
+    """Paged cache of users' latent K = V rows, and attention over it.
+
+    pool [n_pages, page_size, rank] (bfloat16 or float32) and mass (float32
+    [n_pages, page_size], the attention weight every event has collected) are
+    CUDA tensors that the cache references (not copied).  Every call takes the
+    page table (int32 [B, pages]) and the lengths (int32 [B], the call's new
+    events included) of its users; event t of user u lies in row t % page_size
+    of page table[u, t // page_size]."""
+
+    def __init__(self, pool: torch.Tensor, heads: int, mass: Optional[torch.Tensor] = None,
+                 max_batch: int = 1, max_rows: int = 1, max_pages: int = 1):
+        self.lib = load_library()
+        if (not isinstance(pool, torch.Tensor) or not pool.is_cuda or pool.dim() != 3
+                or pool.dtype not in (torch.bfloat16, torch.float32) or not pool.is_contiguous()):
+            raise ValueError("pool must be a contiguous CUDA bfloat16 or float32 "
+                             "[n_pages, page_size, rank] tensor")
+        if mass is not None and (tuple(mass.shape) != tuple(pool.shape[:2])
+                                 or mass.dtype != torch.float32 or mass.device != pool.device
+                                 or not mass.is_contiguous()):
+            raise ValueError("mass must be a contiguous float32 [n_pages, page_size] tensor on "
+                             "the pool's device")
+        self.pool, self.mass, self.heads = pool, mass, int(heads)
+        self.n_pages, self.page_size, self.rank = (int(n) for n in pool.shape)
+        self.device, self.dt = pool.device, pool.dtype
+        c = llatte_cache_dims()
+        c.heads, c.rank, c.page_size, c.n_pages = self.heads, self.rank, self.page_size, self.n_pages
+        c.dtype = LLATTE_BF16 if self.dt == torch.bfloat16 else LLATTE_FP32
+        c.max_batch, c.max_pages, c.max_rows = int(max_batch), int(max_pages), int(max_rows)
+        self.cdims = c
+        h = ctypes.c_void_p()
+        with torch.cuda.device(self.device):
+            rc = self.lib.llatte_cache_create(ctypes.byref(h), ctypes.byref(c), _ptr(pool),
+                                              _ptr(mass))
+        if rc != LLATTE_OK:
+            raise LlatteError(rc, "llatte_cache_create")
+        self.h = h
+
+    def workspace_bytes(self) -> int:
+        return int(self.lib.llatte_cache_workspace_bytes(ctypes.byref(self.cdims)))
+
+    def uses_tensor_cores(self) -> bool:
+        return self.lib.llatte_cache_uses_tensor_cores(self.h) == 1
+
+    def _tensor(self, name, t, dtype, shape):
+        if (not isinstance(t, torch.Tensor) or t.device != self.device or t.dtype != dtype
+                or not t.is_contiguous() or t.dim() != len(shape)
+                or any(n is not None and n != m for n, m in zip(shape, t.shape))):
+            want = ", ".join("*" if n is None else str(n) for n in shape)
+            raise ValueError(f"{name} must be a contiguous {dtype} [{want}] tensor on {self.device}")
+        return t
+
+    def _view(self, table, lengths):
+        self._tensor("lengths", lengths, torch.int32, (None,))
+        B = int(lengths.shape[0])
+        self._tensor("table", table, torch.int32, (B, None))
+        return llatte_cache_view(table=table.data_ptr(), table_stride=int(table.shape[1]),
+                                 lengths=lengths.data_ptr(), B=B), B
+
+    def _on(self, stream, *made):
+        """The stream a call runs on; tensors made here for it are kept until it is done."""
+        if stream is None:
+            return _stream_ptr(torch.cuda.current_stream(self.device))
+        for t in made:
+            if t is not None and isinstance(stream, torch.cuda.Stream):
+                t.record_stream(stream)
+        return _stream_ptr(stream)
+
+    def append(self, x: torch.Tensor, offsets: torch.Tensor, table: torch.Tensor,
+               lengths: torch.Tensor, gain: Optional[torch.Tensor] = None, eps: float = 1e-6,
+               stream=None):
+        """Rows x[offsets[u]:offsets[u + 1]] become user u's newest events (lengths
+        counts them already); with `gain` each is RMS-normalised first."""
+        v, B = self._view(table, lengths)
+        self._tensor("x", x, self.dt, (None, self.rank))
+        self._tensor("offsets", offsets, torch.int64, (B + 1,))
+        if gain is not None:
+            self._tensor("gain", gain, self.dt, (self.rank,))
+        rc = self.lib.llatte_cache_append(self.h, ctypes.byref(v), _ptr(x), int(x.shape[0]),
+                                          _ptr(offsets), _ptr(gain), float(eps), self._on(stream))
+        if rc != LLATTE_OK:
+            raise LlatteError(rc, "llatte_cache_append")
+
+    def attend(self, q: torch.Tensor, q_offsets: torch.Tensor, table: torch.Tensor,
+               lengths: torch.Tensor, n_cand: int = 0, scale: float = 1.0, window: int = 0,
+               n_sink: int = 0, out: Optional[torch.Tensor] = None,
+               lse: Optional[torch.Tensor] = None, accumulate: bool = False,
+               stream=None) -> torch.Tensor:
+        """Attention of the query rows q [rows, heads, rank] over the cache.  User u's
+        rows are q_offsets[u] .. q_offsets[u + 1] - 1: its newest events (already
+        appended), then its last n_cand rows, query tokens that see every event.
+        `window` > 0 limits a row to that many events back from its position and
+        the first n_sink.  `lse` (float32 [rows, heads]) receives the log of the
+        softmax denominators; `accumulate` adds all weights to `mass`."""
+        v, B = self._view(table, lengths)
+        self._tensor("q", q, self.dt, (None, self.heads, self.rank))
+        rows = int(q.shape[0])
+        self._tensor("q_offsets", q_offsets, torch.int64, (B + 1,))
+        made = None
+        if out is None:
+            out = made = torch.empty_like(q)
+        self._tensor("out", out, self.dt, (rows, self.heads, self.rank))
+        if lse is not None:
+            self._tensor("lse", lse, torch.float32, (rows, self.heads))
+        a = llatte_cache_attn(q=q.data_ptr(), q_offsets=q_offsets.data_ptr(), rows=rows,
+                              n_cand=int(n_cand), scale=float(scale), window=int(window),
+                              n_sink=int(n_sink), out=out.data_ptr(),
+                              lse=lse.data_ptr() if lse is not None else None,
+                              accumulate=1 if accumulate else 0)
+        rc = self.lib.llatte_cache_attend(self.h, ctypes.byref(v), ctypes.byref(a),
+                                          self._on(stream, made))
+        if rc != LLATTE_OK:
+            raise LlatteError(rc, "llatte_cache_attend")
+        return out
+
+    def evict(self, table: torch.Tensor, lengths: torch.Tensor, budget: int, n_sink: int = 0,
+              n_recent: int = 0, dst_table: Optional[torch.Tensor] = None,
+              new_lengths: Optional[torch.Tensor] = None, kept: Optional[torch.Tensor] = None,
+              stream=None) -> torch.Tensor:
+        """Keep at most `budget` events per user: the first n_sink, the last n_recent
+        and the heaviest of the others by `mass`, packed in order into the pages
+        of dst_table (default: the user's own first pages).  Returns the new
+        lengths; `kept` (int32 [B, budget]) receives the old slots."""
+        v, B = self._view(table, lengths)
+        made = None
+        if new_lengths is None:
+            new_lengths = made = torch.empty_like(lengths)
+        self._tensor("new_lengths", new_lengths, torch.int32, (B,))
+        if dst_table is not None:
+            self._tensor("dst_table", dst_table, torch.int32, (B, None))
+        if kept is not None:
+            self._tensor("kept", kept, torch.int32, (B, int(budget)))
+        a = llatte_cache_evict_args(
+            budget=int(budget), n_sink=int(n_sink), n_recent=int(n_recent),
+            dst_table=dst_table.data_ptr() if dst_table is not None else None,
+            dst_stride=int(dst_table.shape[1]) if dst_table is not None else 0,
+            new_lengths=new_lengths.data_ptr(),
+            kept=kept.data_ptr() if kept is not None else None)
+        rc = self.lib.llatte_cache_evict(self.h, ctypes.byref(v), ctypes.byref(a),
+                                         self._on(stream, made))
+        if rc != LLATTE_OK:
+            raise LlatteError(rc, "llatte_cache_evict")
+        return new_lengths
+
+    def status(self) -> int:
+        v = ctypes.c_int32(0)
+        rc = self.lib.llatte_cache_get_status(self.h, ctypes.byref(v))
+        if rc not in (LLATTE_OK, LLATTE_ERR_DEVICE):
+            raise LlatteError(rc, "llatte_cache_get_status")
+        return int(v.value)
+
+    def close(self):
+        if getattr(self, "h", None):
+            self.lib.llatte_cache_destroy(self.h)
             self.h = None
 
     def __del__(self):

@@ -1,0 +1,483 @@
+// Paged latent cache: host side of its entry points, and the two operators that
+// move rows: append (RMSNorm of the new latents, written into their pages) and
+// eviction (the heaviest events of every user, packed into fewer pages).
+#include <stdio.h>
+
+#include <algorithm>
+#include <new>
+
+#include "cache.h"
+#include "cache_call.cuh"
+
+using namespace llatte;
+
+struct llatte_cache {
+  llatte_cache_dims dims;
+  int device;
+  int elem;
+  int num_sms;
+  int page_shift;
+  void* pool;            // caller-owned
+  float* mass;           // caller-owned, or NULL
+  char* ws;
+  int32_t* status;
+  int32_t* count;        // [max_batch]
+  int32_t* list;         // [max_batch, max_pages * page_size] kept slots
+  float* lse2;           // [max_rows, heads]
+};
+
+namespace llatte {
+namespace {
+
+// ---------------------------------------------------------------- append
+// c = x / sqrt(mean(x^2) + eps) * g.  One warp per row, its 16-byte vectors
+// spread over the lanes and kept in registers between the sum and the store.
+template <typename T, int NV>
+__global__ void __launch_bounds__(256) cache_append_kernel(CacheAppend a) {
+  constexpr int EV = 16 / sizeof(T);
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const CacheCall& c = a.c;
+  if (row < c.qoff[0] || row >= min(c.rows, c.qoff[c.B])) return;
+  const int u = segment_of(c.qoff, c.B, row);
+  const CacheUser x = cache_user(c, u);
+  if (row < x.row0 || row - x.row0 >= x.n) return;
+  const int32_t slot = x.len - x.n + (int32_t)(row - x.row0);
+  const int64_t dst = cache_row(c, c.table, c.stride, u, slot);
+  if (dst < 0) return;
+  const int nvec = c.r / EV;
+  uint4 v[NV];
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int k = lane + 32 * i;
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (k < nvec) v[i] = __ldg((const uint4*)a.x + row * nvec + k);
+    const T* e = (const T*)&v[i];
+#pragma unroll
+    for (int j = 0; j < EV; ++j) ss = fmaf(to_f(e[j]), to_f(e[j]), ss);
+  }
+  if (a.gain) {
+    const float inv = 1.f / sqrtf(warp_sum(ss) / (float)c.r + a.eps);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int k = lane + 32 * i;
+      if (k >= nvec) continue;
+      const uint4 gv = __ldg((const uint4*)a.gain + k);
+      const T* g = (const T*)&gv;
+      T* e = (T*)&v[i];
+#pragma unroll
+      for (int j = 0; j < EV; ++j) e[j] = from_f<T>(to_f(e[j]) * inv * to_f(g[j]));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int k = lane + 32 * i;
+    if (k < nvec) ((uint4*)a.pool)[dst * nvec + k] = v[i];
+  }
+  if (a.mass && lane == 0) a.mass[dst] = 0.f;
+}
+
+// ---------------------------------------------------------------- evict
+// Masses as unsigned keys in the same order: NaN lowest, -0 equal to +0.
+__device__ __forceinline__ uint32_t mass_key(float f) {
+  if (f != f) return 0u;
+  const uint32_t b = __float_as_uint(f + 0.f);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+constexpr int kSelThreads = 512;
+
+// Kept slots of one user per block.  The threshold, the need-th largest key of
+// the events that do not stay anyway, is found digit by digit (8 bits, from the
+// top) with a histogram of the keys that share the digits found so far; then
+// one pass in slot order writes the kept slots, events at the threshold going
+// to the earliest slots.
+__global__ void __launch_bounds__(kSelThreads) cache_select_kernel(CacheEvict a) {
+  __shared__ int hist[256];
+  __shared__ uint32_t s_prefix;
+  __shared__ int s_need;
+  __shared__ int s_warp[2][kSelThreads / 32];
+  const CacheCall& c = a.c;
+  const int u = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const CacheUser x = cache_user(c, u);
+  const bool left_out = c.lengths[u] != x.len;
+  const int T = x.len, K = a.budget;
+  __syncthreads();                      // new_lengths may be the lengths just read
+  if (left_out) {
+    if (tid == 0) a.count[u] = 0;
+    return;
+  }
+  int32_t* list = a.list + (int64_t)u * a.list_stride;
+  int32_t* kept = a.kept ? a.kept + (int64_t)u * K : nullptr;
+  if (tid == 0) {
+    a.count[u] = min(T, K);
+    a.new_lengths[u] = min(T, K);
+  }
+  if (T <= K) {
+    for (int t = tid; t < T; t += kSelThreads) {
+      list[t] = t;
+      if (kept) kept[t] = t;
+    }
+    return;
+  }
+  const int lo = c.n_sink, hi = T - a.n_recent;       // [lo, hi): may go
+  auto key_of = [&](int t) -> uint32_t {
+    const int64_t row = cache_row(c, c.table, c.stride, u, t);
+    return row < 0 ? 0u : mass_key(a.mass[row]);
+  };
+  if (tid == 0) { s_prefix = 0; s_need = K - c.n_sink - a.n_recent; }
+  __syncthreads();
+  const bool any = s_need > 0;
+  for (int shift = 24; any && shift >= 0; shift -= 8) {
+    for (int i = tid; i < 256; i += kSelThreads) hist[i] = 0;
+    __syncthreads();
+    const uint32_t prefix = s_prefix;
+    for (int t = lo + tid; t < hi; t += kSelThreads) {
+      const uint32_t k = key_of(t);
+      if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8)))
+        atomicAdd(&hist[(k >> shift) & 255], 1);
+    }
+    __syncthreads();
+    if (tid == 0) {
+      int need = s_need, d = 255;
+      while (hist[d] < need) need -= hist[d--];
+      s_need = need;
+      s_prefix = prefix | ((uint32_t)d << shift);
+    }
+    __syncthreads();
+  }
+  const uint32_t thr = s_prefix;
+  const int n_eq = s_need;              // events at the threshold that stay
+  int base_eq = 0, base = 0;
+  for (int t0 = 0; t0 < T; t0 += kSelThreads) {
+    const int t = t0 + tid;
+    bool eq = false, keep = false;
+    if (t < T) {
+      if (t < lo || t >= hi) {
+        keep = true;
+      } else if (any) {
+        const uint32_t k = key_of(t);
+        keep = k > thr;
+        eq = k == thr;
+      }
+    }
+    uint32_t b = __ballot_sync(0xffffffffu, eq);
+    if (lane == 0) s_warp[0][warp] = __popc(b);
+    __syncthreads();
+    int before = base_eq + __popc(b & ((1u << lane) - 1));
+    for (int w = 0; w < kSelThreads / 32; ++w) {
+      if (w < warp) before += s_warp[0][w];
+      base_eq += s_warp[0][w];
+    }
+    if (eq && before < n_eq) keep = true;
+    b = __ballot_sync(0xffffffffu, keep);
+    if (lane == 0) s_warp[1][warp] = __popc(b);
+    __syncthreads();
+    int at = base + __popc(b & ((1u << lane) - 1));
+    for (int w = 0; w < kSelThreads / 32; ++w) {
+      if (w < warp) at += s_warp[1][w];
+      base += s_warp[1][w];
+    }
+    if (keep) {
+      list[at] = t;
+      if (kept) kept[at] = t;
+    }
+    __syncthreads();
+  }
+}
+
+// Moves the kept rows.  A block owns one 64-byte column slice of one user's
+// rows (the last slice index: the masses) and walks them in order, so that
+// packing in place is safe without any other block: row i comes from a slot
+// >= i, and a step's rows are all read before any of them is written.
+constexpr int kMoveThreads = 256;
+constexpr int kSliceBytes = 64;
+
+__global__ void __launch_bounds__(kMoveThreads)
+cache_move_kernel(CacheEvict a, int row_bytes, int slices) {
+  const CacheCall& c = a.c;
+  const int u = blockIdx.y, slice = blockIdx.x;
+  const int n = a.count[u];
+  const int32_t* list = a.list + (int64_t)u * a.list_stride;
+  const bool in_place = a.dst_table == c.table;
+  if (slice == slices) {
+    for (int i0 = 0; i0 < n; i0 += kMoveThreads) {
+      const int i = i0 + threadIdx.x;
+      float v = 0.f;
+      int64_t dst = -1;
+      if (i < n) {
+        const int t = list[i];
+        const int64_t src = cache_row(c, c.table, c.stride, u, t);
+        dst = in_place && t == i ? -1 : cache_row(c, a.dst_table, a.dst_stride, u, i);
+        v = src < 0 ? 0.f : a.mass[src];
+      }
+      __syncthreads();
+      if (dst >= 0) a.mass[dst] = v;
+    }
+    return;
+  }
+  const int vec = threadIdx.x % (kSliceBytes / 16);
+  const int byte = slice * kSliceBytes + vec * 16;
+  constexpr int ROWS = kMoveThreads / (kSliceBytes / 16);
+  for (int i0 = 0; i0 < n; i0 += ROWS) {
+    const int i = i0 + threadIdx.x / (kSliceBytes / 16);
+    uint4 v = make_uint4(0, 0, 0, 0);
+    int64_t dst = -1;
+    if (i < n && byte < row_bytes) {
+      const int t = list[i];
+      const int64_t src = cache_row(c, c.table, c.stride, u, t);
+      dst = in_place && t == i ? -1 : cache_row(c, a.dst_table, a.dst_stride, u, i);
+      if (src >= 0) v = *(const uint4*)((const char*)a.pool + src * row_bytes + byte);
+    }
+    __syncthreads();
+    if (dst >= 0) *(uint4*)((char*)a.pool + dst * row_bytes + byte) = v;
+  }
+}
+
+template <typename T>
+cudaError_t append_t(const CacheAppend& a, cudaStream_t s) {
+  const unsigned blocks = (unsigned)((a.c.rows + 7) / 8);
+  const int nvec = a.c.r * (int)sizeof(T) / 16;
+  if (nvec <= 32) cache_append_kernel<T, 1><<<blocks, 256, 0, s>>>(a);
+  else cache_append_kernel<T, 2><<<blocks, 256, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache_append(int elem, const CacheAppend& a, cudaStream_t s) {
+  return elem == 4 ? append_t<float>(a, s) : append_t<__nv_bfloat16>(a, s);
+}
+
+cudaError_t launch_cache_evict(int elem, const CacheEvict& a, cudaStream_t s) {
+  cache_select_kernel<<<a.c.B, kSelThreads, 0, s>>>(a);
+  const int row_bytes = a.c.r * elem;
+  const int slices = (row_bytes + kSliceBytes - 1) / kSliceBytes;
+  cache_move_kernel<<<dim3(slices + 1, a.c.B), kMoveThreads, 0, s>>>(a, row_bytes, slices);
+  return cudaGetLastError();
+}
+
+}  // namespace llatte
+
+// ---------------------------------------------------------------- host side
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
+
+int check_cache_dims(const llatte_cache_dims* d) {
+  if (!d) return LLATTE_ERR_ARG;
+  if (d->dtype != LLATTE_BF16 && d->dtype != LLATTE_FP32) return LLATTE_ERR_ARG;
+  if (d->heads <= 0 || d->rank <= 0 || d->n_pages <= 0 || d->max_batch <= 0 ||
+      d->max_pages <= 0 || d->max_rows <= 0)
+    return LLATTE_ERR_ARG;
+  const int e = d->dtype == LLATTE_BF16 ? 2 : 4;
+  if (d->page_size != 16 && d->page_size != 32 && d->page_size != 64 && d->page_size != 128)
+    return LLATTE_ERR_UNSUPPORTED;
+  if (d->rank * e % 16 != 0 || d->rank > 256) return LLATTE_ERR_UNSUPPORTED;
+  if (d->max_batch > LLATTE_CACHE_MAX_BATCH) return LLATTE_ERR_UNSUPPORTED;
+  const int64_t top = (int64_t)1 << 31;
+  if ((int64_t)d->n_pages * d->page_size >= top || (int64_t)d->max_pages * d->page_size >= top)
+    return LLATTE_ERR_UNSUPPORTED;
+  if (d->max_rows >= top || d->max_rows * d->heads >= top) return LLATTE_ERR_UNSUPPORTED;
+  return LLATTE_OK;
+}
+
+struct CacheLayout { size_t status, count, list, lse2, total; };
+
+CacheLayout cache_layout(const llatte_cache_dims& d) {
+  CacheLayout L;
+  size_t o = 0;
+  auto take = [&](size_t bytes) { size_t r = o; o += align_up(bytes); return r; };
+  L.status = take(sizeof(int32_t));
+  L.count = take(sizeof(int32_t) * d.max_batch);
+  L.list = take(sizeof(int32_t) * (size_t)d.max_batch * d.max_pages * d.page_size);
+  L.lse2 = take(sizeof(float) * (size_t)d.max_rows * d.heads);
+  L.total = o;
+  return L;
+}
+
+// Makes the cache's device current for one call.
+struct DeviceGuard {
+  int prev = -1;
+  bool ok;
+  explicit DeviceGuard(int device) {
+    ok = cudaGetDevice(&prev) == cudaSuccess;
+    if (ok && prev != device) ok = cudaSetDevice(device) == cudaSuccess;
+    else prev = -1;
+  }
+  ~DeviceGuard() { if (prev >= 0) cudaSetDevice(prev); }
+};
+
+int check_view(const llatte_cache* h, const llatte_cache_view* v) {
+  if (!h || !v) return LLATTE_ERR_ARG;
+  if (v->B < 0 || v->B > h->dims.max_batch) return LLATTE_ERR_ARG;
+  if (v->B > 0 && (!v->table || !v->lengths || v->table_stride <= 0)) return LLATTE_ERR_ARG;
+  return LLATTE_OK;
+}
+
+CacheCall make_call(const llatte_cache* h, const llatte_cache_view* v, const int64_t* qoff,
+                    int64_t rows) {
+  CacheCall c = {};
+  c.table = v->table; c.stride = v->table_stride; c.lengths = v->lengths; c.B = v->B;
+  c.qoff = qoff; c.rows = rows;
+  c.cap = (int64_t)std::min(v->table_stride, h->dims.max_pages) * h->dims.page_size;
+  c.n_pages = h->dims.n_pages; c.page_shift = h->page_shift;
+  c.heads = h->dims.heads; c.r = h->dims.rank; c.status = h->status;
+  return c;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t llatte_cache_workspace_bytes(const llatte_cache_dims* dims) {
+  if (check_cache_dims(dims) != LLATTE_OK) return 0;
+  return cache_layout(*dims).total;
+}
+
+int llatte_cache_create(llatte_cache** out, const llatte_cache_dims* dims, void* pool,
+                        float* mass) {
+  if (!out) return LLATTE_ERR_ARG;
+  *out = nullptr;
+  const int rc = check_cache_dims(dims);
+  if (rc != LLATTE_OK) return rc;
+  if (!pool || ((uintptr_t)pool & 15) || ((uintptr_t)mass & 3)) return LLATTE_ERR_ARG;
+  for (const void* p : {(const void*)pool, (const void*)mass}) {
+    if (!p) continue;
+    cudaPointerAttributes at;
+    if (cudaPointerGetAttributes(&at, p) != cudaSuccess ||
+        (at.type != cudaMemoryTypeDevice && at.type != cudaMemoryTypeManaged)) {
+      cudaGetLastError();
+      return LLATTE_ERR_ARG;    // the pools must be device memory
+    }
+  }
+  llatte_cache* h = new (std::nothrow) llatte_cache();
+  if (!h) return LLATTE_ERR_OOM;
+  h->dims = *dims;
+  h->elem = dims->dtype == LLATTE_BF16 ? 2 : 4;
+  h->pool = pool;
+  h->mass = mass;
+  h->page_shift = 0;
+  while ((1 << h->page_shift) < dims->page_size) ++h->page_shift;
+  if (cudaGetDevice(&h->device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device) !=
+          cudaSuccess) {
+    llatte_cache_destroy(h);
+    return LLATTE_ERR_CUDA;
+  }
+  const CacheLayout L = cache_layout(*dims);
+  if (cudaMalloc((void**)&h->ws, L.total) != cudaSuccess) {
+    cudaGetLastError();
+    h->ws = nullptr;
+    llatte_cache_destroy(h);
+    return LLATTE_ERR_OOM;
+  }
+  h->status = (int32_t*)(h->ws + L.status);
+  h->count = (int32_t*)(h->ws + L.count);
+  h->list = (int32_t*)(h->ws + L.list);
+  h->lse2 = (float*)(h->ws + L.lse2);
+  if (cudaMemset(h->ws, 0, L.total) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
+    llatte_cache_destroy(h);
+    return LLATTE_ERR_CUDA;
+  }
+  *out = h;
+  return LLATTE_OK;
+}
+
+int llatte_cache_append(llatte_cache* h, const llatte_cache_view* v, const void* x, int64_t rows,
+                        const int64_t* offsets, const void* gain, float eps, void* stream) {
+  const int rc = check_view(h, v);
+  if (rc != LLATTE_OK) return rc;
+  if (rows < 0 || rows * (int64_t)h->dims.heads >= (int64_t)1 << 31) return LLATTE_ERR_ARG;
+  if (v->B == 0 || rows == 0) return LLATTE_OK;
+  if (!x || !offsets || (((uintptr_t)x | (uintptr_t)gain) & 15)) return LLATTE_ERR_ARG;
+  if (gain && !(eps > 0.f)) return LLATTE_ERR_ARG;
+  DeviceGuard g(h->device);
+  if (!g.ok) return LLATTE_ERR_CUDA;
+  CacheAppend a = {};
+  a.c = make_call(h, v, offsets, rows);
+  a.pool = h->pool; a.mass = h->mass; a.x = x; a.gain = gain; a.eps = eps;
+  return launch_cache_append(h->elem, a, (cudaStream_t)stream) == cudaSuccess ? LLATTE_OK
+                                                                             : LLATTE_ERR_CUDA;
+}
+
+int llatte_cache_attend(llatte_cache* h, const llatte_cache_view* v, const llatte_cache_attn* p,
+                        void* stream) {
+  const int rc = check_view(h, v);
+  if (rc != LLATTE_OK) return rc;
+  if (!p || p->rows < 0 || p->rows > h->dims.max_rows || p->n_cand < 0 || p->window < 0 ||
+      p->n_sink < 0 || (p->accumulate != 0 && p->accumulate != 1) || !(p->scale == p->scale))
+    return LLATTE_ERR_ARG;
+  if (p->accumulate && !h->mass) return LLATTE_ERR_ARG;
+  if (v->B == 0 || p->rows == 0) return LLATTE_OK;
+  if (!p->q || !p->out || !p->q_offsets || (((uintptr_t)p->q | (uintptr_t)p->out) & 15))
+    return LLATTE_ERR_ARG;
+  DeviceGuard g(h->device);
+  if (!g.ok) return LLATTE_ERR_CUDA;
+  CacheAttn a = {};
+  a.c = make_call(h, v, p->q_offsets, p->rows);
+  a.c.n_cand = p->n_cand; a.c.window = p->window; a.c.n_sink = p->n_sink;
+  a.pool = h->pool; a.mass = h->mass; a.q = p->q; a.out = p->out; a.lse = p->lse;
+  a.lse2 = p->accumulate ? h->lse2 : nullptr;
+  a.scale2 = p->scale * kLog2e;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (launch_cache_attn_simt(h->elem, a, s) != cudaSuccess) return LLATTE_ERR_CUDA;
+  if (p->accumulate && launch_cache_mass_simt(h->elem, a, s) != cudaSuccess)
+    return LLATTE_ERR_CUDA;
+  return LLATTE_OK;
+}
+
+int llatte_cache_evict(llatte_cache* h, const llatte_cache_view* v,
+                       const llatte_cache_evict_args* p, void* stream) {
+  const int rc = check_view(h, v);
+  if (rc != LLATTE_OK) return rc;
+  if (!p || p->budget < 1 || p->n_sink < 0 || p->n_recent < 0 ||
+      (int64_t)p->n_sink + p->n_recent > p->budget || !h->mass)
+    return LLATTE_ERR_ARG;
+  if (v->B == 0) return LLATTE_OK;
+  if (!p->new_lengths || (p->dst_table && p->dst_stride <= 0)) return LLATTE_ERR_ARG;
+  // a destination row must be able to name the pages of every kept event
+  const int64_t cap = (int64_t)std::min(v->table_stride, h->dims.max_pages) * h->dims.page_size;
+  const int64_t most = std::min<int64_t>(p->budget, cap);
+  if (p->dst_table && (int64_t)p->dst_stride * h->dims.page_size < most) return LLATTE_ERR_ARG;
+  DeviceGuard g(h->device);
+  if (!g.ok) return LLATTE_ERR_CUDA;
+  CacheEvict a = {};
+  a.c = make_call(h, v, nullptr, 0);
+  a.c.n_sink = p->n_sink;
+  a.pool = h->pool; a.mass = h->mass; a.budget = p->budget; a.n_recent = p->n_recent;
+  a.dst_table = p->dst_table ? p->dst_table : v->table;
+  a.dst_stride = p->dst_table ? p->dst_stride : v->table_stride;
+  a.new_lengths = p->new_lengths; a.kept = p->kept;
+  a.list = h->list; a.list_stride = (int64_t)h->dims.max_pages * h->dims.page_size;
+  a.count = h->count;
+  return launch_cache_evict(h->elem, a, (cudaStream_t)stream) == cudaSuccess ? LLATTE_OK
+                                                                            : LLATTE_ERR_CUDA;
+}
+
+int llatte_cache_get_status(llatte_cache* h, int32_t* device_status) {
+  if (!h || !device_status) return LLATTE_ERR_ARG;
+  DeviceGuard g(h->device);
+  int32_t v = 0;
+  if (!g.ok || cudaDeviceSynchronize() != cudaSuccess ||
+      cudaMemcpy(&v, h->status, sizeof(v), cudaMemcpyDeviceToHost) != cudaSuccess ||
+      cudaMemset(h->status, 0, sizeof(int32_t)) != cudaSuccess)
+    return LLATTE_ERR_CUDA;
+  *device_status = v;
+  return v ? LLATTE_ERR_DEVICE : LLATTE_OK;
+}
+
+int llatte_cache_uses_tensor_cores(const llatte_cache* h) { return h ? 0 : LLATTE_ERR_ARG; }
+
+void llatte_cache_destroy(llatte_cache* h) {
+  if (!h) return;
+  DeviceGuard g(h->device);
+  cudaDeviceSynchronize();
+  cudaFree(h->ws);
+  delete h;
+}
+
+}  // extern "C"

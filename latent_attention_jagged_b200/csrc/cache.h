@@ -1,0 +1,66 @@
+// Internal interface of the paged latent cache (not part of the C ABI).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/llatte.h"
+
+namespace llatte {
+
+// One call's users and rows, as the kernels see them.
+struct CacheCall {
+  const int32_t* table;      // [B, stride] page ids
+  const int32_t* lengths;    // [B] cached events, new ones included
+  const int64_t* qoff;       // [B + 1] rows of every user (NULL: no rows, evict)
+  int64_t rows;              // rows of the arrays behind qoff
+  int64_t cap;               // most events of a user: pages a table row can name * page size
+  int32_t stride, B;
+  int32_t n_pages, page_shift;   // page size = 1 << page_shift
+  int32_t heads, r;
+  int32_t n_cand, window, n_sink;
+  int32_t* status;
+};
+
+struct CacheAttn {
+  CacheCall c;
+  const void* pool;          // [n_pages, page, r]
+  float* mass;               // [n_pages, page] or NULL
+  const void* q;             // [rows, h, r]
+  void* out;                 // [rows, h, r]
+  float* lse;                // [rows, h] natural log, or NULL
+  float* lse2;               // [rows, h] log2 units, workspace (needed when accumulating)
+  float scale2;              // scale * log2(e): scores in log2 units
+};
+
+struct CacheAppend {
+  CacheCall c;
+  void* pool;
+  float* mass;               // or NULL
+  const void* x;             // [rows, r]
+  const void* gain;          // [r] or NULL
+  float eps;
+};
+
+struct CacheEvict {
+  CacheCall c;
+  void* pool;
+  float* mass;
+  int budget, n_recent;      // c.n_sink first events
+  const int32_t* dst_table; int32_t dst_stride;   // == table when in place
+  int32_t* new_lengths;
+  int32_t* kept;             // [B, budget] or NULL
+  int32_t* list;             // workspace: [B, list_stride] kept slots
+  int64_t list_stride;
+  int32_t* count;            // workspace: [B] kept events, -1 = nothing to move
+};
+
+cudaError_t launch_cache_append(int elem, const CacheAppend& a, cudaStream_t s);
+cudaError_t launch_cache_evict(int elem, const CacheEvict& a, cudaStream_t s);
+// CUDA-core attention (any rank up to 256, both types) and its accumulation.
+cudaError_t launch_cache_attn_simt(int elem, const CacheAttn& a, cudaStream_t s);
+cudaError_t launch_cache_mass_simt(int elem, const CacheAttn& a, cudaStream_t s);
+
+}  // namespace llatte
