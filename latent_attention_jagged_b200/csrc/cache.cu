@@ -1,13 +1,13 @@
 // Paged latent cache: host side of its entry points, and the two operators that
 // move rows: append (RMSNorm of the new latents, written into their pages) and
 // eviction (the heaviest events of every user, packed into fewer pages).
-#include <stdio.h>
-
 #include <algorithm>
+#include <cmath>
 #include <new>
 
 #include "cache.h"
 #include "cache_call.cuh"
+#include "tc_gemm.h"
 
 using namespace llatte;
 
@@ -24,6 +24,11 @@ struct llatte_cache {
   int32_t* count;        // [max_batch]
   int32_t* list;         // [max_batch, max_pages * page_size] kept slots
   float* lse2;           // [max_rows, heads]
+  bool tc;               // attention on the tensor cores
+  CUtensorMap tmC;       // the pool, a page a box (tc)
+  float* part_o;         // [2 num_sms, kCacheBlockRows, rank] (tc)
+  float2* part_ml;       // [2 num_sms, kCacheBlockRows]
+  CacheJoin* join;       // [num_sms]
 };
 
 namespace llatte {
@@ -285,16 +290,30 @@ int check_cache_dims(const llatte_cache_dims* d) {
   return LLATTE_OK;
 }
 
-struct CacheLayout { size_t status, count, list, lse2, total; };
+bool cache_uses_tc(const llatte_cache_dims& d) {
+  return d.dtype == LLATTE_BF16 && cache_attn_tc_supported(d.rank);
+}
+
+struct CacheLayout { size_t status, count, list, lse2, part_o, part_ml, join, total; };
+
+// The parts' slots are counted for the largest part there is (148 SMs); a device
+// with more SMs runs as many CTAs as there are slots.
+constexpr int kCacheCtas = 148;
 
 CacheLayout cache_layout(const llatte_cache_dims& d) {
-  CacheLayout L;
+  CacheLayout L = {};
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t r = o; o += align_up(bytes); return r; };
   L.status = take(sizeof(int32_t));
   L.count = take(sizeof(int32_t) * d.max_batch);
   L.list = take(sizeof(int32_t) * (size_t)d.max_batch * d.max_pages * d.page_size);
   L.lse2 = take(sizeof(float) * (size_t)d.max_rows * d.heads);
+  if (cache_uses_tc(d)) {
+    const size_t slots = (size_t)2 * kCacheCtas * kCacheBlockRows;
+    L.part_o = take(sizeof(float) * slots * d.rank);
+    L.part_ml = take(sizeof(float2) * slots);
+    L.join = take(sizeof(CacheJoin) * kCacheCtas);
+  }
   L.total = o;
   return L;
 }
@@ -379,6 +398,18 @@ int llatte_cache_create(llatte_cache** out, const llatte_cache_dims* dims, void*
   h->count = (int32_t*)(h->ws + L.count);
   h->list = (int32_t*)(h->ws + L.list);
   h->lse2 = (float*)(h->ws + L.lse2);
+  h->num_sms = std::min(h->num_sms, kCacheCtas);
+  h->tc = cache_uses_tc(*dims);
+  if (h->tc) {
+    h->part_o = (float*)(h->ws + L.part_o);
+    h->part_ml = (float2*)(h->ws + L.part_ml);
+    h->join = (CacheJoin*)(h->ws + L.join);
+    if (!make_tmap_bf16(&h->tmC, pool, (uint64_t)dims->n_pages * dims->page_size, dims->rank,
+                        dims->page_size)) {
+      llatte_cache_destroy(h);
+      return LLATTE_ERR_CUDA;
+    }
+  }
   if (cudaMemset(h->ws, 0, L.total) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
     llatte_cache_destroy(h);
     return LLATTE_ERR_CUDA;
@@ -409,7 +440,7 @@ int llatte_cache_attend(llatte_cache* h, const llatte_cache_view* v, const llatt
   const int rc = check_view(h, v);
   if (rc != LLATTE_OK) return rc;
   if (!p || p->rows < 0 || p->rows > h->dims.max_rows || p->n_cand < 0 || p->window < 0 ||
-      p->n_sink < 0 || (p->accumulate != 0 && p->accumulate != 1) || !(p->scale == p->scale))
+      p->n_sink < 0 || (p->accumulate != 0 && p->accumulate != 1) || !std::isfinite(p->scale * kLog2e))
     return LLATTE_ERR_ARG;
   if (p->accumulate && !h->mass) return LLATTE_ERR_ARG;
   if (v->B == 0 || p->rows == 0) return LLATTE_OK;
@@ -424,7 +455,10 @@ int llatte_cache_attend(llatte_cache* h, const llatte_cache_view* v, const llatt
   a.lse2 = p->accumulate ? h->lse2 : nullptr;
   a.scale2 = p->scale * kLog2e;
   cudaStream_t s = (cudaStream_t)stream;
-  if (launch_cache_attn_simt(h->elem, a, s) != cudaSuccess) return LLATTE_ERR_CUDA;
+  a.part_o = h->part_o; a.part_ml = h->part_ml; a.join = h->join;
+  const cudaError_t e = h->tc ? launch_cache_attn_tc(a, h->tmC, h->num_sms, s)
+                              : launch_cache_attn_simt(h->elem, a, s);
+  if (e != cudaSuccess) return LLATTE_ERR_CUDA;
   if (p->accumulate && launch_cache_mass_simt(h->elem, a, s) != cudaSuccess)
     return LLATTE_ERR_CUDA;
   return LLATTE_OK;
@@ -470,7 +504,7 @@ int llatte_cache_get_status(llatte_cache* h, int32_t* device_status) {
   return v ? LLATTE_ERR_DEVICE : LLATTE_OK;
 }
 
-int llatte_cache_uses_tensor_cores(const llatte_cache* h) { return h ? 0 : LLATTE_ERR_ARG; }
+int llatte_cache_uses_tensor_cores(const llatte_cache* h) { return h ? h->tc : LLATTE_ERR_ARG; }
 
 void llatte_cache_destroy(llatte_cache* h) {
   if (!h) return;

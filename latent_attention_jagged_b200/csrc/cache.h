@@ -24,6 +24,13 @@ struct CacheCall {
   int32_t* status;
 };
 
+// A block of (row, head) pairs that one CTA began and others went on with: its
+// first pair, rows and parts (rows = 0: none).
+struct CacheJoin {
+  int64_t pair0;
+  int32_t rows, parts;
+};
+
 struct CacheAttn {
   CacheCall c;
   const void* pool;          // [n_pages, page, r]
@@ -32,6 +39,10 @@ struct CacheAttn {
   void* out;                 // [rows, h, r]
   float* lse;                // [rows, h] natural log, or NULL
   float* lse2;               // [rows, h] log2 units, workspace (needed when accumulating)
+  // workspaces for blocks that are summed from parts: two slots per CTA
+  float* part_o;             // [2 CTAs, block rows, r] unnormalised sums
+  float2* part_ml;           // [2 CTAs, block rows] maximum (log2 units) and sum
+  CacheJoin* join;           // [CTAs]
   float scale2;              // scale * log2(e): scores in log2 units
 };
 
@@ -59,6 +70,12 @@ struct CacheEvict {
 
 cudaError_t launch_cache_append(int elem, const CacheAppend& a, cudaStream_t s);
 cudaError_t launch_cache_evict(int elem, const CacheEvict& a, cudaStream_t s);
+// Tensor-core attention (bf16, rank 64, 128 or 256); tmC: the pool as a tensor
+// [n_pages * page, r] in boxes of a page.
+bool cache_attn_tc_supported(int r);
+cudaError_t launch_cache_attn_tc(const CacheAttn& a, const CUtensorMap& tmC, int num_sms,
+                                 cudaStream_t s);
+constexpr int kCacheBlockRows = 128;       // largest block of pairs
 // CUDA-core attention (any rank up to 256, both types) and its accumulation.
 cudaError_t launch_cache_attn_simt(int elem, const CacheAttn& a, cudaStream_t s);
 cudaError_t launch_cache_mass_simt(int elem, const CacheAttn& a, cudaStream_t s);

@@ -14,18 +14,14 @@ struct CacheUser {
   int32_t len;       // cached events
 };
 
-// User u of the call; a user the header leaves out (bad offsets or length) gets
-// no rows and no events, and its fault goes to the status word.
-__device__ __forceinline__ CacheUser cache_user(const CacheCall& c, int u) {
+// A user of the call from its offsets and length; a user the header leaves out
+// (bad offsets or length) gets no rows and no events, and its fault goes to the
+// status word.
+__device__ __forceinline__ CacheUser cache_user_of(const CacheCall& c, int64_t a, int64_t b,
+                                                   int32_t len) {
   CacheUser x = {0, 0, 0, 0};
-  const int32_t len = c.lengths[u];
   int bad = (len < 0 || len > c.cap) ? LLATTE_DEV_TOO_LONG : 0;
-  int64_t a = 0, b = 0;
-  if (c.qoff) {
-    a = c.qoff[u];
-    b = c.qoff[u + 1];
-    if (a < 0 || b < a || b > c.rows) bad |= LLATTE_DEV_BAD_OFFSETS;
-  }
+  if (a < 0 || b < a || b > c.rows) bad |= LLATTE_DEV_BAD_OFFSETS;
   if (!bad) {
     x.row0 = a;
     x.n = (int32_t)(b - a);
@@ -38,6 +34,15 @@ __device__ __forceinline__ CacheUser cache_user(const CacheCall& c, int u) {
   }
   if (bad) atomicOr(c.status, bad);
   return x;
+}
+
+__device__ __forceinline__ CacheUser cache_user(const CacheCall& c, int u) {
+  int64_t a = 0, b = 0;
+  if (c.qoff) {
+    a = c.qoff[u];
+    b = c.qoff[u + 1];
+  }
+  return cache_user_of(c, a, b, c.lengths[u]);
 }
 
 // Last event that row j of the user may see (-1: none).
