@@ -459,8 +459,10 @@ int llatte_cache_attend(llatte_cache* h, const llatte_cache_view* v, const llatt
   const cudaError_t e = h->tc ? launch_cache_attn_tc(a, h->tmC, h->num_sms, s)
                               : launch_cache_attn_simt(h->elem, a, s);
   if (e != cudaSuccess) return LLATTE_ERR_CUDA;
-  if (p->accumulate && launch_cache_mass_simt(h->elem, a, s) != cudaSuccess)
-    return LLATTE_ERR_CUDA;
+  if (!p->accumulate) return LLATTE_OK;
+  const cudaError_t m = h->tc ? launch_cache_mass_tc(a, h->tmC, h->num_sms, s)
+                              : launch_cache_mass_simt(h->elem, a, s);
+  if (m != cudaSuccess) return LLATTE_ERR_CUDA;
   return LLATTE_OK;
 }
 

@@ -75,6 +75,8 @@ cudaError_t launch_cache_evict(int elem, const CacheEvict& a, cudaStream_t s);
 bool cache_attn_tc_supported(int r);
 cudaError_t launch_cache_attn_tc(const CacheAttn& a, const CUtensorMap& tmC, int num_sms,
                                  cudaStream_t s);
+cudaError_t launch_cache_mass_tc(const CacheAttn& a, const CUtensorMap& tmC, int num_sms,
+                                 cudaStream_t s);
 constexpr int kCacheBlockRows = 128;       // largest block of pairs
 // CUDA-core attention (any rank up to 256, both types) and its accumulation.
 cudaError_t launch_cache_attn_simt(int elem, const CacheAttn& a, cudaStream_t s);

@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(32 * Cfg<R, MT>::WARPS, 1)
 cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmC,
                   const CacheAttn p, const int min_quota) {
   using C = Cfg<R, MT>;
+  using Line = ByRows<MT, KT>;
   constexpr int KP = C::KP, RSUB = C::RSUB, KS = C::KS, OBUF = C::OBUF, QBUF = C::QBUF;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -160,7 +161,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   }
   // everything below reads what earlier kernels wrote
   pdl_wait();
-  cache_split<MT, KT>(c, min_quota, (int32_t*)sKV, split);
+  cache_split<Line>(c, min_quota, (int32_t*)sKV, split);
   fence_proxy_async_smem();               // the ring's next writes come from TMA
   tc_fence_before();
   __syncthreads();
@@ -177,17 +178,18 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     const int32_t P = 1 << c.page_shift;
     const int np = KT >> c.page_shift;
     const int32_t outside = c.n_pages << c.page_shift;
-    CacheItems<MT, KT> items;
+    CacheItems<Line> items;
     items.start(c, run);
     CacheItem it;
     bool ok = true;
     while (ok && items.next(c, it)) {
-      if (it.tiles == 0) continue;
+      const CacheBlock blk = cache_block<MT, KT>(c, it.x, it.b);
+      if (it.x.len == 0) continue;
       const int32_t* row = c.table + (int64_t)it.u * c.stride;
       // pool row of this lane's page in tile i of the piece
       auto place = [&](int i) -> int32_t {
-        const int32_t t = cache_tile(it.k, i) * KT + lane * P;
-        if (lane >= np || !cache_seen(c, it.k, t, t + P)) return outside;
+        const int32_t t = cache_tile(blk, i) * KT + lane * P;
+        if (lane >= np || !cache_seen(c, blk, t, t + P)) return outside;
         const int32_t page = __ldg(row + (t >> c.page_shift));
         if ((uint32_t)page < (uint32_t)c.n_pages) return page << c.page_shift;
         atomicOr(c.status, LLATTE_DEV_BAD_ID);
@@ -288,11 +290,11 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         pend.valid = false;
         return true;
       };
-      CacheItems<MT, KT> items;
+      CacheItems<Line> items;
       items.start(c, run);
       CacheItem it;
       while (ok && items.next(c, it)) {
-        if (it.tiles == 0) continue;
+        if (it.x.len == 0) continue;
         const int ob = itm % OBUF, qb = itm % QBUF;
         if (QBUF == 1 && !flush()) break;
         if (!mbar_wait(&q_full[qb], (itm / QBUF) & 1, abort_flag, c.status)) break;
@@ -321,17 +323,18 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     const float2 mul2 = make_float2(mul, mul);
     uint32_t g = 0, itm = 0, pphase = 0;
     bool ok = true;
-    CacheItems<MT, KT> items;
+    CacheItems<Line> items;
     items.start(c, run);
     CacheItem it;
     while (ok && items.next(c, it)) {
-      if (it.tiles == 0) continue;
+      const CacheBlock blk = cache_block<MT, KT>(c, it.x, it.b);
+      if (it.x.len == 0) continue;
       const int ob = itm % OBUF;
       const uint32_t o_col = ob * R + part * (R / 2);          // this warp's half of O
       const uint32_t pairs = (uint32_t)it.x.n * (uint32_t)c.heads;
       const uint32_t pair = (uint32_t)it.b * MT + row;
       const bool valid = pair < pairs;
-      const int32_t pos = valid ? cache_pos(it.x, (int)(pair / (uint32_t)c.heads)) : it.k.pmax;
+      const int32_t pos = valid ? cache_pos(it.x, (int)(pair / (uint32_t)c.heads)) : blk.pmax;
       const int32_t low = cache_low(c, pos);
       const bool idle = (uint32_t)it.b * MT + quad * 32 >= pairs;   // no row in this quadrant
       float m_run = -INFINITY, l_run = 0.f;     // running maximum (log2 units), partial sum
@@ -345,7 +348,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         }
         tc_fence_after();
         const uint32_t s_addr = lane_base + C::S_COL + (g & 1) * KT + part * KP;
-        const int32_t tile0 = cache_tile(it.k, i) * KT;
+        const int32_t tile0 = cache_tile(blk, i) * KT;
         float v[KP];
         tmem_ld64(s_addr, v);
         if (p.scale2 <= 0.f) {
@@ -354,7 +357,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
           for (int k = 0; k < KP; ++k) v[k] *= f;
         }
         // some row hides some event of the tile (the same answer in every warp)
-        if (it.k.pmin < tile0 + KT - 1 || cache_low(c, it.k.pmax) > tile0) {
+        if (blk.pmin < tile0 + KT - 1 || cache_low(c, blk.pmax) > tile0) {
           const int64_t t0 = tile0 + part * KP;
           uint64_t vis = bits_below((int64_t)pos + 1 - t0);
           if (c.window > 0) vis &= ~bits_below(low - t0) | bits_below(c.n_sink - t0);
@@ -478,7 +481,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     const bool writer = warp == C::EPI0 && lane == 0;
     if (writer) join->rows = 0;
     uint32_t itm = 0;
-    CacheItems<MT, KT> items;
+    CacheItems<Line> items;
     items.start(c, run);
     CacheItem it;
     while (items.next(c, it)) {
@@ -488,7 +491,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       const bool idle = (uint32_t)it.b * MT + quad * 32 >= pairs;
       const int64_t at = it.x.row0 * c.heads + pair;
       __nv_bfloat16* orow = valid ? (__nv_bfloat16*)p.out + at * R : nullptr;
-      if (it.tiles == 0) {                 // no event: zeros
+      if (it.x.len == 0) {                 // no event: zeros
         if (idle) continue;
         const uint4 z[4] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0),
                             make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};

@@ -1,0 +1,386 @@
+// Accumulated attention weights over the paged latent cache for sm_100a (bf16,
+// rank 64, 128 or 256): after the attention kernel has left every row's log sum,
+//
+//   mass_t += sum over rows i and heads that see t of exp(scale q_i . c_t - lse_i).
+//
+// The weights of a row are known only after its last tile, so the scores are
+// computed again, transposed: S^T = C Q^T with the tile's 128 events on the M = 128
+// lanes of tensor memory and NP (row, head) pairs on its columns.  One thread then
+// owns an event and sums its columns in registers: no exchange between threads, no
+// atomics inside a call, and a fixed order (pairs ascending).  An event's row of
+// S^T depends on its own latent alone, so what is stored beside it cannot reach it.
+//
+// One item = a tile of one user and a run of the blocks of pairs that see it; a
+// tile cut between CTAs is summed from parts by a second kernel.
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "cache.h"
+#include "cache_call.cuh"
+#include "cache_sched.cuh"
+#include "tc_common.cuh"
+#include "tc_drain.cuh"
+#include "tc_gemm.h"
+
+namespace llatte {
+
+using namespace tc;
+
+namespace {
+
+constexpr int KT = 128;
+
+template <int R, int NP>
+struct Cfg {
+  static constexpr int RSUB = R / 64;
+  static constexpr int CP = NP / 2;                    // pairs of a softmax warp
+  static constexpr int SB = 4;                         // S^T buffers in tensor memory
+  // ring slots: single tokens reread the events, long chunks the queries
+  static constexpr int KS = NP == 32 ? (R == 256 ? 3 : 6) : (R == 256 ? 1 : 2);
+  static constexpr int QS = NP == 32 ? (R == 256 ? 2 : 4) : (R == 256 ? 2 : 4);
+  static constexpr uint32_t KSUB = KT * 128, K_BYTES = RSUB * KSUB;
+  static constexpr uint32_t QSUB = NP * 128, Q_BYTES = RSUB * QSUB;
+  static constexpr uint32_t BAR_BYTES = R == 256 ? 256 : 384;
+  static constexpr uint32_t F_BYTES = 8 * CP * 8 + 128 * 4;   // log sums, positions; sums
+  static constexpr size_t SMEM = 1024 + KS * K_BYTES + QS * Q_BYTES + BAR_BYTES + F_BYTES;
+  static constexpr uint32_t TMEM_COLS = SB * NP;
+  static_assert(SMEM <= 232448, "shared memory budget");
+  static_assert(TMEM_COLS <= 512, "TMEM budget");
+  static_assert(KS * K_BYTES >= 4 * (LLATTE_CACHE_MAX_BATCH + 1), "prefix sums");
+  static_assert(KS * K_BYTES + QS * Q_BYTES <= 229376, "rings");
+};
+
+constexpr int kSoft0 = 2, kSoft = 8;
+constexpr int kThreads = 32 * (kSoft0 + kSoft);
+
+template <int CP>
+__device__ __forceinline__ void tmem_ld_cp(uint32_t taddr, float (&v)[CP]) {
+  if constexpr (CP == 64) {
+    tmem_ld64(taddr, v);
+  } else {
+    static_assert(CP == 16, "column counts");
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+  }
+}
+
+template <int R, int NP>
+__global__ void __launch_bounds__(kThreads, 1)
+cache_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmC,
+                  const CacheAttn p) {
+  using C = Cfg<R, NP>;
+  using Line = ByTiles<NP, KT>;
+  constexpr int CP = C::CP, RSUB = C::RSUB, KS = C::KS, QS = C::QS, SB = C::SB;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* sK = smem;
+  uint8_t* sQ = sK + KS * C::K_BYTES;
+  uint64_t* bars = (uint64_t*)(sQ + QS * C::Q_BYTES);
+  uint64_t* k_full = bars;                 // [KS]
+  uint64_t* k_empty = k_full + KS;         // [KS]
+  uint64_t* q_full = k_empty + KS;         // [QS]
+  uint64_t* q_empty = q_full + QS;         // [QS]
+  uint64_t* s_full = q_empty + QS;         // [SB]
+  uint64_t* s_empty = s_full + SB;         // [SB] every softmax warp has read S^T
+  uint64_t* pair_bar = s_empty + SB;       // [4] the two softmax warps of a lane quadrant
+  uint64_t* drain = pair_bar + 4;
+  uint32_t* tmem_slot = (uint32_t*)(drain + 1);
+  volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
+  CacheSplit* split = (CacheSplit*)(tmem_slot + 2);
+  static_assert((2 * KS + 2 * QS + 2 * SB + 5) * 8 + 8 + sizeof(CacheSplit) <= C::BAR_BYTES,
+                "barriers");
+  float* sums = (float*)((uint8_t*)bars + C::BAR_BYTES);   // [128]
+  float* lbuf = sums + 128;                                  // [8 warps][CP] log sums
+  int32_t* pbuf = (int32_t*)(lbuf + 8 * CP);                 // [8 warps][CP] positions
+
+  pdl_trigger();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const CacheCall& c = p.c;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < KS; ++s) { mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 1); }
+    for (int s = 0; s < QS; ++s) { mbar_init(&q_full[s], 1); mbar_init(&q_empty[s], 1); }
+    for (int s = 0; s < SB; ++s) { mbar_init(&s_full[s], 1); mbar_init(&s_empty[s], kSoft); }
+    for (int q = 0; q < 4; ++q) mbar_init(&pair_bar[q], 2);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmC);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  cache_split<Line>(c, 1, (int32_t*)sK, split);
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const CacheSplit run = *split;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    uint32_t kn = 0, qn = 0;               // tiles and blocks of pairs asked for
+    const int32_t P = 1 << c.page_shift;
+    const int np = KT >> c.page_shift;
+    const int32_t outside = c.n_pages << c.page_shift;
+    CacheItems<Line> items;
+    items.start(c, run);
+    CacheItem it;
+    bool ok = true;
+    while (ok && items.next(c, it)) {
+      const CacheBlock all = cache_all<KT>(c, it.x);
+      const int32_t tile = cache_tile(all, it.b);
+      int32_t y = outside;
+      const int32_t t = tile * KT + lane * P;
+      if (lane < np && cache_seen(c, all, t, t + P)) {
+        const int32_t page = __ldg(c.table + (int64_t)it.u * c.stride + (t >> c.page_shift));
+        if ((uint32_t)page < (uint32_t)c.n_pages) y = page << c.page_shift;
+        else atomicOr(c.status, LLATTE_DEV_BAD_ID);
+      }
+      const int ks = kn % KS;
+      if (lane == 0) {
+        ok = mbar_wait(&k_empty[ks], ((kn / KS) & 1) ^ 1, abort_flag, c.status);
+        if (ok) mbar_arrive_expect_tx(&k_full[ks], C::K_BYTES);
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      if (lane < np) {
+#pragma unroll
+        for (int s = 0; s < RSUB; ++s)
+          tma_load_2d(&tmC, &k_full[ks], sK + ks * C::K_BYTES + s * C::KSUB + lane * P * 128,
+                      s * 64, y);
+      }
+      ++kn;
+      if (lane == 0) {
+        const int b0 = Line::range(c, it.x, tile).x;
+        for (int i = it.t0; i < it.t1; ++i, ++qn) {
+          const int qs = qn % QS;
+          if (!mbar_wait(&q_empty[qs], ((qn / QS) & 1) ^ 1, abort_flag, c.status)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&q_full[qs], C::Q_BYTES);
+          const int32_t qrow = (int32_t)(it.x.row0 * c.heads + (int64_t)(b0 + i) * NP);
+#pragma unroll
+          for (int s = 0; s < RSUB; ++s)
+            tma_load_2d(&tmQ, &q_full[qs], sQ + qs * C::Q_BYTES + s * C::QSUB, s * 64, qrow);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+    __syncwarp();
+    if (lane == 0 && *abort_flag) {
+      drain_ring(k_full, KS, kn, c.status);
+      drain_ring(q_full, QS, qn, c.status);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t IDESC = idesc_bf16(128, NP, false, false);
+      uint32_t kn = 0, qn = 0;
+      bool ok = true;
+      CacheItems<Line> items;
+      items.start(c, run);
+      CacheItem it;
+      while (ok && items.next(c, it)) {
+        const int ks = kn % KS;
+        if (!mbar_wait(&k_full[ks], (kn / KS) & 1, abort_flag, c.status)) break;
+        const uint32_t k_addr = smem_u32(sK + ks * C::K_BYTES);
+        for (int i = it.t0; i < it.t1; ++i, ++qn) {
+          const int qs = qn % QS, sb = qn % SB;
+          if (!mbar_wait(&q_full[qs], (qn / QS) & 1, abort_flag, c.status) ||
+              !mbar_wait(&s_empty[sb], ((qn / SB) & 1) ^ 1, abort_flag, c.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t q_addr = smem_u32(sQ + qs * C::Q_BYTES);
+#pragma unroll
+          for (int k = 0; k < R / 16; ++k) {
+            const uint64_t ad = sdesc_sw128(k_addr + (k >> 2) * C::KSUB + (k & 3) * 32, 16, 1024);
+            const uint64_t bd = sdesc_sw128(q_addr + (k >> 2) * C::QSUB + (k & 3) * 32, 16, 1024);
+            umma_bf16(tmem + sb * NP, ad, bd, IDESC, k > 0 ? 1u : 0u);
+          }
+          umma_commit(&s_full[sb]);
+          umma_commit(&q_empty[qs]);
+        }
+        if (ok) umma_commit(&k_empty[ks]);
+        ++kn;
+      }
+      umma_commit(drain);
+      int dummy = 0;
+      mbar_wait(drain, 0, &dummy, c.status);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int quad = warp & 3, part = (warp - kSoft0) >> 2;   // event quadrant, half of the pairs
+    const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
+    float* lw = lbuf + (warp - kSoft0) * CP;
+    int32_t* pw = pbuf + (warp - kSoft0) * CP;
+    CacheJoin* join = p.join + blockIdx.x;
+    const bool writer = warp == kSoft0 && lane == 0;
+    if (writer) join->rows = 0;
+    uint32_t qn = 0, pphase = 0;
+    bool ok = true;
+    CacheItems<Line> items;
+    items.start(c, run);
+    CacheItem it;
+    while (ok && items.next(c, it)) {
+      const CacheBlock all = cache_all<KT>(c, it.x);
+      const int32_t tile0 = cache_tile(all, it.b) * KT;
+      const int32_t t = tile0 + quad * 32 + lane;          // this lane's event
+      const uint32_t pairs = (uint32_t)it.x.n * (uint32_t)c.heads;
+      const int b0 = Line::range(c, it.x, tile0 / KT).x;
+      float sum = 0.f;
+      for (int i = it.t0; i < it.t1; ++i, ++qn) {
+        const int sb = qn % SB;
+        // this warp's pairs: log sums and positions, one or two a lane
+        const uint32_t pair0 = (uint32_t)(b0 + i) * NP + part * CP;
+        __syncwarp();
+#pragma unroll
+        for (int k = lane; k < CP; k += 32) {
+          const uint32_t pair = pair0 + k;
+          const bool in = pair < pairs;
+          lw[k] = in ? p.lse2[it.x.row0 * c.heads + pair] : 0.f;
+          pw[k] = in ? cache_pos(it.x, (int)(pair / (uint32_t)c.heads)) : -1;
+        }
+        __syncwarp();
+        bool w = mbar_wait(&s_full[sb], (qn / SB) & 1, abort_flag, c.status);
+        if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
+        tc_fence_after();
+        float v[CP];
+        tmem_ld_cp<CP>(lane_base + sb * NP + part * CP, v);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_empty[sb]);
+        if (pair0 >= pairs) continue;
+        float s4[4] = {0.f, 0.f, 0.f, 0.f};
+        // every pair here sees every event of the quadrant?
+        const int32_t first = pw[0], last = pw[CP - 1];
+        const bool full = last >= tile0 + quad * 32 + 31 && pair0 + CP <= pairs &&
+                          (c.window == 0 || cache_low(c, last) <= tile0 + quad * 32) &&
+                          first >= tile0 + quad * 32 + 31;
+        if (full) {
+#pragma unroll
+          for (int k = 0; k < CP; k += 4) {
+            const float4 l4 = *(const float4*)(lw + k);
+            s4[0] += ex2_approx(fmaf(v[k], p.scale2, -l4.x));
+            s4[1] += ex2_approx(fmaf(v[k + 1], p.scale2, -l4.y));
+            s4[2] += ex2_approx(fmaf(v[k + 2], p.scale2, -l4.z));
+            s4[3] += ex2_approx(fmaf(v[k + 3], p.scale2, -l4.w));
+          }
+        } else {
+          const bool sink = t < c.n_sink || c.window == 0;
+#pragma unroll
+          for (int k = 0; k < CP; ++k) {
+            const int32_t pos = pw[k];
+            const bool see = t <= pos && (sink || t > pos - c.window);
+            const float e = ex2_approx(fmaf(v[k], p.scale2, -lw[k]));
+            s4[k & 3] += see ? e : 0.f;
+          }
+        }
+        sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+      }
+      if (!ok) break;
+      // the two halves of the pairs meet
+      if (part == 1) sums[quad * 32 + lane] = sum;
+      if (!group_sync(&pair_bar[quad], pphase, abort_flag, c.status)) break;
+      if (part == 0) {
+        sum += sums[quad * 32 + lane];
+        if (!it.whole) {
+          p.part_ml[((int64_t)blockIdx.x * 2 + (it.starts ? 1 : 0)) * KT + quad * 32 + lane].x = sum;
+        } else if (t <= all.pmax && (t >= cache_low(c, all.pmin) || t < c.n_sink)) {
+          const int64_t at = cache_row(c, c.table, c.stride, it.u, t);
+          if (at >= 0) atomicAdd(&p.mass[at], sum);
+        }
+      }
+      if (!group_sync(&pair_bar[quad], pphase, abort_flag, c.status)) break;
+      if (writer && !it.whole && it.starts) {
+        join->pair0 = ((int64_t)it.u << 32) | (uint32_t)tile0;
+        join->parts = it.parts;
+        join->rows = min(KT, all.pmax + 1 - tile0);
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// The tile that CTA blockIdx.x of the accumulation kernel began and did not finish:
+// its parts in order of the pairs, one thread per event.
+__global__ void __launch_bounds__(KT) cache_mass_join_kernel(const CacheAttn p) {
+  pdl_trigger();
+  pdl_wait();
+  const CacheJoin j = p.join[blockIdx.x];
+  if ((int)threadIdx.x >= j.rows) return;
+  const CacheCall& c = p.c;
+  const int u = (int)(j.pair0 >> 32);
+  const int32_t t = (int32_t)(uint32_t)j.pair0 + threadIdx.x;
+  const CacheBlock all = cache_all<KT>(c, cache_user(c, u));
+  if (!(t >= cache_low(c, all.pmin) || t < c.n_sink)) return;
+  float sum = 0.f;
+  for (int i = 0; i < j.parts; ++i)
+    sum += p.part_ml[((int64_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * KT + threadIdx.x].x;
+  const int64_t at = cache_row(c, c.table, c.stride, u, t);
+  if (at >= 0) atomicAdd(&p.mass[at], sum);
+}
+
+template <int R, int NP>
+cudaError_t launch_rn(const CacheAttn& a, const CUtensorMap& tmC, int num_sms, cudaStream_t s) {
+  using C = Cfg<R, NP>;
+  static uint64_t attr_devices = 0;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (!(attr_devices >> (dev & 63) & 1)) {
+    cudaError_t e = cudaFuncSetAttribute(cache_mass_kernel<R, NP>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+    if (e != cudaSuccess) return e;
+    attr_devices |= 1ull << (dev & 63);
+  }
+  CUtensorMap tmQ;
+  if (!make_tmap_bf16(&tmQ, a.q, (uint64_t)a.c.rows * a.c.heads, R, NP))
+    return cudaErrorInvalidValue;
+  cudaError_t e = launch_dependent(cache_mass_kernel<R, NP>, dim3(num_sms), dim3(kThreads),
+                                   C::SMEM, s, 1, tmQ, tmC, a);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(cache_mass_join_kernel, dim3(num_sms), dim3(KT), 0, s, 1, a);
+}
+
+template <int R>
+cudaError_t launch_r(const CacheAttn& a, const CUtensorMap& tmC, int num_sms, cudaStream_t s) {
+  if (a.c.rows * a.c.heads <= 32 * (int64_t)a.c.B) return launch_rn<R, 32>(a, tmC, num_sms, s);
+  return launch_rn<R, 128>(a, tmC, num_sms, s);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_mass_tc(const CacheAttn& a, const CUtensorMap& tmC, int num_sms,
+                                 cudaStream_t s) {
+  switch (a.c.r) {
+    case 64: return launch_r<64>(a, tmC, num_sms, s);
+    case 128: return launch_r<128>(a, tmC, num_sms, s);
+    case 256: return launch_r<256>(a, tmC, num_sms, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace llatte

@@ -50,14 +50,56 @@ __device__ __forceinline__ bool cache_seen(const CacheCall& c, const CacheBlock&
   return t0 <= k.pmax && (t1 > cache_low(c, k.pmin) || t0 < c.n_sink);
 }
 
-// Places in the line that a block takes: its tiles, or one when it has none
-// (its rows still get their zeros).
-__device__ __forceinline__ int32_t cache_places(const CacheBlock& k) { return max(1, k.tiles); }
+// The line of the attention kernels: blocks of MT pairs; a block takes a place for
+// each of its tiles, or one when it has none (its rows still get their zeros).
+template <int MT, int KT>
+struct ByRows {
+  __device__ __forceinline__ static int blocks(const CacheCall& c, const CacheUser& x) {
+    return (int)(((uint32_t)x.n * (uint32_t)c.heads + (MT - 1)) / MT);
+  }
+  __device__ __forceinline__ static int32_t places(const CacheCall& c, const CacheUser& x, int b) {
+    return max(1, cache_block<MT, KT>(c, x, b).tiles);
+  }
+};
 
-template <int MT>
-__device__ __forceinline__ int cache_blocks(const CacheCall& c, const CacheUser& x) {
-  return (int)(((uint32_t)x.n * (uint32_t)c.heads + (MT - 1)) / MT);
+// The events that any row of a user reads, as one block.
+template <int KT>
+__device__ __forceinline__ CacheBlock cache_all(const CacheCall& c, const CacheUser& x) {
+  CacheBlock k;
+  k.pmin = cache_pos(x, 0);
+  k.pmax = x.len - 1;
+  const int32_t all = k.pmax < 0 ? 0 : k.pmax / KT + 1;
+  k.first_tile = cache_low(c, k.pmin) / KT;
+  const int32_t sink = min(c.n_sink, k.pmax + 1);
+  k.sink_tiles = sink <= 0 ? 0 : min((sink - 1) / KT + 1, k.first_tile);
+  k.tiles = x.n == 0 ? 0 : k.sink_tiles + (all - min(k.first_tile, all));
+  return k;
 }
+
+// The line of the accumulation kernel: blocks are a user's tiles of KT events; a
+// block takes a place for each block of NP pairs with a row that sees the tile.
+template <int NP, int KT>
+struct ByTiles {
+  __device__ __forceinline__ static int blocks(const CacheCall& c, const CacheUser& x) {
+    return cache_all<KT>(c, x).tiles;
+  }
+  // First and last block of pairs that sees tile `tile`.  The rows that see it lie
+  // between the first one at or after its start and the last one whose window
+  // reaches back to its end.
+  __device__ __forceinline__ static int2 range(const CacheCall& c, const CacheUser& x,
+                                               int32_t tile) {
+    const int64_t t0 = (int64_t)tile * KT, start = x.len - x.m;
+    int64_t lo = max((int64_t)0, t0 - start), hi = x.n - 1;
+    const int64_t last = t0 + KT - 2 + c.window;       // last position that sees its end
+    if (c.window > 0 && t0 >= c.n_sink && x.len - 1 > last) hi = last - start;
+    return make_int2((int)((uint32_t)lo * (uint32_t)c.heads / NP),
+                     (int)(((uint32_t)hi * (uint32_t)c.heads + c.heads - 1) / NP));
+  }
+  __device__ __forceinline__ static int32_t places(const CacheCall& c, const CacheUser& x, int b) {
+    const int2 r = range(c, x, cache_tile(cache_all<KT>(c, x), b));
+    return r.y - r.x + 1;
+  }
+};
 
 // Where a CTA's run of places lies.
 struct CacheSplit {
@@ -69,7 +111,7 @@ struct CacheSplit {
 // in the block.  A cut inside a block that is short against a CTA's run moves to
 // the nearer end of the block: the imbalance is at most an eighth of a run, and
 // the block need not be summed from parts.
-template <int MT, int KT>
+template <class W>
 __device__ __forceinline__ void cache_cut(const CacheCall& c, const int32_t* prefix, int64_t at,
                                           int64_t base, int32_t quota, CacheSplit* s) {
   const int lane = threadIdx.x & 31;
@@ -84,11 +126,11 @@ __device__ __forceinline__ void cache_cut(const CacheCall& c, const int32_t* pre
   }
   s->u = lo;
   const CacheUser x = cache_user(c, lo);
-  const int nb = cache_blocks<MT>(c, x);
+  const int nb = W::blocks(c, x);
   int32_t left = (int32_t)at - prefix[lo];
   for (int b0 = 0; b0 < nb; b0 += 32) {
     const int b = b0 + lane;
-    const int32_t own = b < nb ? cache_places(cache_block<MT, KT>(c, x, b)) : 0;
+    const int32_t own = b < nb ? W::places(c, x, b) : 0;
     int32_t v = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -119,7 +161,7 @@ __device__ __forceinline__ void cache_cut(const CacheCall& c, const int32_t* pre
 // Every thread of the CTA calls this (it synchronises); prefix has B + 1 entries
 // of shared memory, prefix[u] = places before user u.  A call of 2^31 places or
 // more gets no work and LLATTE_DEV_TOO_LONG.
-template <int MT, int KT>
+template <class W>
 __device__ __forceinline__ void cache_split(const CacheCall& c, int min_quota, int32_t* prefix,
                                             CacheSplit* out) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
@@ -129,10 +171,10 @@ __device__ __forceinline__ void cache_split(const CacheCall& c, int min_quota, i
     const int u = u0 + lane;
     CacheUser x = {0, 0, 0, 0};
     if (u < c.B) x = cache_user(c, u);
-    const int nb = cache_blocks<MT>(c, x);
+    const int nb = W::blocks(c, x);
     int64_t places = 0;
     if (nb <= 4)
-      for (int b = 0; b < nb; ++b) places += cache_places(cache_block<MT, KT>(c, x, b));
+      for (int b = 0; b < nb; ++b) places += W::places(c, x, b);
     // users of many blocks: the whole warp, one block per lane
     for (uint32_t big = __ballot_sync(0xffffffffu, nb > 4); big; big &= big - 1) {
       const int l = __ffs(big) - 1;
@@ -143,7 +185,7 @@ __device__ __forceinline__ void cache_split(const CacheCall& c, int min_quota, i
       y.len = __shfl_sync(0xffffffffu, x.len, l);
       const int nby = __shfl_sync(0xffffffffu, nb, l);
       int64_t sum = 0;
-      for (int b = lane; b < nby; b += 32) sum += cache_places(cache_block<MT, KT>(c, y, b));
+      for (int b = lane; b < nby; b += 32) sum += W::places(c, y, b);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       if (lane == l) places = sum;
@@ -174,9 +216,9 @@ __device__ __forceinline__ void cache_split(const CacheCall& c, int min_quota, i
     CacheSplit s, e;
     s.quota = (int32_t)max((int64_t)min_quota, (base + gridDim.x - 1) / gridDim.x);
     const int64_t first = (int64_t)blockIdx.x * s.quota;
-    cache_cut<MT, KT>(c, prefix, min(first, base), base, s.quota, &s);
+    cache_cut<W>(c, prefix, min(first, base), base, s.quota, &s);
     e.quota = s.quota;
-    cache_cut<MT, KT>(c, prefix, min(first + s.quota, base), base, s.quota, &e);
+    cache_cut<W>(c, prefix, min(first + s.quota, base), base, s.quota, &e);
     s.end = e.begin;
     if (lane == 0) *out = s;
   }
@@ -187,17 +229,15 @@ __device__ __forceinline__ void cache_split(const CacheCall& c, int min_quota, i
 struct CacheItem {
   int32_t u, b;
   CacheUser x;
-  CacheBlock k;
-  int32_t t0, t1;              // places; equal to tiles unless the block has none
-  int32_t tiles;               // tiles of this piece
+  int32_t t0, t1;
   bool whole;                  // the block is not cut
-  int32_t first_cta, parts;    // CTAs first_cta .. first_cta + parts - 1 share it
   bool starts;                 // it starts in this CTA
+  int32_t parts;               // CTAs that share it
 };
 
 // Walks the pieces of this CTA's run.  The next user's offsets and length are
 // loaded one user ahead, so that no role waits for them.
-template <int MT, int KT>
+template <class W>
 struct CacheItems {
   int32_t pos, end, quota, u, b, t;
   CacheUser x;
@@ -220,7 +260,7 @@ struct CacheItems {
     if (pos < end) {
       fetch(c, u);
       x = cache_user_of(c, next_a, next_b, next_len);
-      nb = cache_blocks<MT>(c, x);
+      nb = W::blocks(c, x);
       fetch(c, u + 1);
     }
   }
@@ -231,20 +271,17 @@ struct CacheItems {
       if (u >= c.B) return false;
       b = 0;
       x = cache_user_of(c, next_a, next_b, next_len);
-      nb = cache_blocks<MT>(c, x);
+      nb = W::blocks(c, x);
       fetch(c, u + 1);
     }
     it.u = u; it.b = b; it.x = x;
-    it.k = cache_block<MT, KT>(c, x, b);
-    const int32_t places = cache_places(it.k);
+    const int32_t places = W::places(c, x, b);
     it.t0 = t;
     it.t1 = min(places, t + (end - pos));
     const int32_t g0 = pos - t;             // the block's first place in the line
     it.whole = it.t0 == 0 && it.t1 == places;
-    it.first_cta = g0 / quota;
-    it.parts = (g0 + places - 1) / quota - it.first_cta + 1;
+    it.parts = (g0 + places - 1) / quota - g0 / quota + 1;
     it.starts = it.t0 == 0;
-    it.tiles = it.k.tiles == 0 ? 0 : it.t1 - it.t0;
     pos += it.t1 - it.t0;
     t = 0;
     ++b;
