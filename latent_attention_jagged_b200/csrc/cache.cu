@@ -404,8 +404,8 @@ int llatte_cache_create(llatte_cache** out, const llatte_cache_dims* dims, void*
     h->part_o = (float*)(h->ws + L.part_o);
     h->part_ml = (float2*)(h->ws + L.part_ml);
     h->join = (CacheJoin*)(h->ws + L.join);
-    if (!make_tmap_bf16(&h->tmC, pool, (uint64_t)dims->n_pages * dims->page_size, dims->rank,
-                        dims->page_size)) {
+    const uint64_t rows = (uint64_t)dims->n_pages * dims->page_size;
+    if (!make_tmap_bf16(&h->tmC, pool, rows, dims->rank, std::min(dims->page_size, kCacheBox))) {
       llatte_cache_destroy(h);
       return LLATTE_ERR_CUDA;
     }

@@ -43,6 +43,8 @@ struct CacheAttn {
   float* part_o;             // [2 CTAs, block rows, r] unnormalised sums
   float2* part_ml;           // [2 CTAs, block rows] maximum (log2 units) and sum
   CacheJoin* join;           // [CTAs]
+  int32_t min_quota;         // fewest tiles of a CTA's run
+  bool never_cut;            // no block is cut between CTAs (then there is nothing to join)
   float scale2;              // scale * log2(e): scores in log2 units
 };
 
@@ -71,12 +73,18 @@ struct CacheEvict {
 cudaError_t launch_cache_append(int elem, const CacheAppend& a, cudaStream_t s);
 cudaError_t launch_cache_evict(int elem, const CacheEvict& a, cudaStream_t s);
 // Tensor-core attention (bf16, rank 64, 128 or 256); tmC: the pool as a tensor
-// [n_pages * page, r] in boxes of a page.
+// [n_pages * page, r] in boxes of a page or kCacheBox rows.
 bool cache_attn_tc_supported(int r);
 cudaError_t launch_cache_attn_tc(const CacheAttn& a, const CUtensorMap& tmC, int num_sms,
                                  cudaStream_t s);
 cudaError_t launch_cache_mass_tc(const CacheAttn& a, const CUtensorMap& tmC, int num_sms,
                                  cudaStream_t s);
+// Its form for blocks of 16 pairs, and the sum of the blocks that were cut (mt: rows
+// of a block).
+cudaError_t launch_cache_token(const CacheAttn& a, const CUtensorMap& tmC, int num_sms,
+                               cudaStream_t s);
+cudaError_t launch_cache_join(const CacheAttn& a, int mt, int num_sms, cudaStream_t s);
+constexpr int kCacheBox = 64;              // rows of a box of tmC, or a page if that is smaller
 constexpr int kCacheBlockRows = 128;       // largest block of pairs
 // CUDA-core attention (any rank up to 256, both types) and its accumulation.
 cudaError_t launch_cache_attn_simt(int elem, const CacheAttn& a, cudaStream_t s);

@@ -31,7 +31,6 @@
 #include "cache_sched.cuh"
 #include "tc_common.cuh"
 #include "tc_drain.cuh"
-#include "tc_epilogue.cuh"
 #include "tc_gemm.h"
 
 namespace llatte {
@@ -42,126 +41,186 @@ namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int KT = 128;                   // events of a tile
+constexpr int HT = KT / 2;                // events of a half
+constexpr int NG = 4;                     // softmax groups, half S buffers
+
+// Six warpgroups: producer (warp 0), issuers of S (warp 1) and of P C (warp 2); four of
+// softmax; the epilogue.  The launch's 80 registers a thread are dealt out again: 128 threads x
+// (56 + 4 x 80 + 104) = 768 x 80 (softmax keeps what it has).
+constexpr int kThreads = 768;
+constexpr int kRegsIssue = 56, kRegsSoft = 80, kRegsEpi = 104;
+static_assert(kRegsIssue + NG * kRegsSoft + kRegsEpi <= 480, "registers of the launch");
+template <int N> __device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 template <int R, int MT>
 struct Cfg {
   static constexpr bool SMALL = MT == 32;
-  static constexpr int KP = KT / 2;                    // events of a softmax warp
   static constexpr int RSUB = R / 64;
-  static constexpr int OBUF = (2 * R + 2 * KT <= 512) ? 2 : 1;
+  static constexpr int OBUF = (2 * R + NG * HT <= 512) ? 2 : 1;
   static constexpr int QBUF = SMALL || R <= 128 ? 2 : 1;
-  static constexpr int KS = SMALL ? (R == 256 ? 3 : R == 128 ? 6 : 8) : (R == 256 ? 2 : 4);
+  static constexpr int KS = SMALL ? (R == 256 ? 6 : 12) : (R == 256 ? 4 : R == 128 ? 8 : 12);   // halves in the ring
   static constexpr uint32_t QSUB = MT * 128;           // one 64-wide sub-tile of a query block
   static constexpr uint32_t Q_BYTES = RSUB * QSUB;
-  static constexpr uint32_t KV_SUB = KT * 128;
-  static constexpr uint32_t KV_BYTES = RSUB * KV_SUB;
+  // The ring: for each 64 columns KS halves of 64 rows, so that the halves of a tile
+  // (slots 2 j and 2 j + 1) are 128 rows of one operand.
+  static constexpr uint32_t H_SUB = HT * 128;
+  static constexpr uint32_t H_BYTES = RSUB * H_SUB;
+  static constexpr uint32_t KV_SUB = KS * H_SUB;
+  static_assert(KS % 2 == 0 && KS >= NG, "halves of a tile are neighbours");
   static constexpr uint32_t S_COL = OBUF * R;
-  // warps: MT = 128: producer 0, MMA 1, softmax 2..9, epilogue 10..13.  MT = 32:
-  // softmax 0 and 4 (TMEM lanes 0..31 belong to warps 0 mod 4), producer 1,
-  // MMA 2, epilogue 8.
-  static constexpr int WARPS = SMALL ? 9 : 14;
-  static constexpr int PROD = SMALL ? 1 : 0, MMA = SMALL ? 2 : 1;
-  static constexpr int NSOFT = SMALL ? 2 : 8, EPI0 = SMALL ? 8 : 10, NEPI = SMALL ? 1 : 4;
-  static constexpr uint32_t BAR_BYTES = 512;
-  static constexpr uint32_t F_BYTES = 4 * MT * 8;      // sums, maxima, partial maxima
-  static constexpr uint32_t STAGE = SMALL ? 0 : kStageBytes;
-  static constexpr size_t SMEM = 1024 + QBUF * Q_BYTES + (size_t)KS * KV_BYTES + BAR_BYTES +
-                                 F_BYTES + NEPI * STAGE;
+  static constexpr int NQ = SMALL ? 1 : 4;             // TMEM lane quadrants in use
+  static constexpr uint32_t BAR_BYTES = R == 256 ? 512 : 576;
+  static constexpr uint32_t F_BYTES = (OBUF * 2 + 1) * NG * MT * 4;   // sums, maxima
+  static constexpr size_t SMEM = 1024 + QBUF * Q_BYTES + (size_t)KS * H_BYTES + BAR_BYTES +
+                                 F_BYTES;
   static_assert(SMEM <= 232448, "shared memory budget");
-  static_assert(OBUF * R + 2 * KT <= 512, "TMEM budget");
+  static_assert(OBUF * R + NG * HT <= 512, "TMEM budget");
   // an M = 128 product reads 16 KB from the start of a 32-row sub-tile
-  static_assert(!SMALL || KS * KV_BYTES >= 16384, "operand reads stay in the buffers");
-  // the split's prefix sums lie in the ring before its first load
-  static_assert(KS * KV_BYTES >= 4 * (LLATTE_CACHE_MAX_BATCH + 1), "prefix sums");
+  static_assert(!SMALL || KS * H_BYTES >= 16384, "operand reads stay in the buffers");
+  // the split works in the ring before its first load
+  static_assert(KS * H_BYTES >= sizeof(CacheSplitSpace), "split");
 };
 
-// TMEM column (relative to the S buffer) of the packed bf16 P for events
-// [16 kk, 16 kk + 16): each softmax warp packs its half into the first columns of
-// its half of the buffer.
-template <int KP>
-__device__ __forceinline__ uint32_t p_col(int kk) {
-  const int key = 16 * kk;
-  return (uint32_t)((key / KP) * KP + (key % KP) / 2);
+// 2^x for two values on the FMA pipe: x = j + f with j = rint(x), 2^f from the
+// polynomial of degree 5 with the least maximum relative error on [-1/2, 1/2]
+// (7.5e-8; 2.1e-7 with fp32 rounding, 2^-22), j added to the exponent field.
+// x <= -125 gives 0, as a hidden score must; NaN stays NaN.
+__device__ __forceinline__ float2 exp2_fma(float2 x) {
+  constexpr float kRound = 12582912.f;  // 1.5 * 2^23: j in the low bits of the sum
+  auto two = [](float v) { return make_float2(v, v); };
+  const float2 t = add_f2(x, two(kRound));
+  const float2 f = fma_f2(add_f2(t, two(-kRound)), two(-1.f), x);
+  float2 e = fma_f2(two(0x1.5c08e6p-10f), f, two(0x1.3d0c52p-7f));
+  e = fma_f2(e, f, two(0x1.c6b6e4p-5f));
+  e = fma_f2(e, f, two(0x1.ebf918p-3f));
+  e = fma_f2(e, f, two(0x1.62e428p-1f));
+  e = fma_f2(e, f, two(0x1.000002p+0f));
+  float2 r;
+  r.x = __uint_as_float(__float_as_uint(e.x) + (__float_as_uint(t.x) << 23));
+  r.y = __uint_as_float(__float_as_uint(e.y) + (__float_as_uint(t.y) << 23));
+  r.x = x.x <= -125.f ? 0.f : x.x != x.x ? x.x : r.x;
+  r.y = x.y <= -125.f ? 0.f : x.y != x.y ? x.y : r.y;
+  return r;
 }
 
-// Bits [lo, hi) of 64, both clamped.
-__device__ __forceinline__ uint64_t bits_below(int64_t n) {
-  return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
+// One warp clears the latents of half a tile that are not finite, so that a weight of
+// 0 hides them (several warps may do so at once: they write the same zeros).
+template <int R>
+__device__ __forceinline__ void clear_rows(uint8_t* kv, uint32_t sub) {
+  for (int k = threadIdx.x & 31; k < HT; k += 32) {
+    bool bad = false;
+    for (int s = 0; s < R / 64; ++s) {
+      const uint4* e = (const uint4*)(kv + s * sub + k * 128);
+      for (int j = 0; j < 8; ++j) {
+        const uint4 x = e[j];
+        for (uint32_t y : {x.x, x.y, x.z, x.w})
+          bad |= (y & 0x7f80u) == 0x7f80u || (y & 0x7f800000u) == 0x7f800000u;
+      }
+    }
+    if (!bad) continue;
+    for (int s = 0; s < R / 64; ++s)
+      for (int j = 0; j < 8; ++j) ((uint4*)(kv + s * sub + k * 128))[j] = make_uint4(0, 0, 0, 0);
+  }
+  fence_proxy_async_smem();
 }
 
-// The 64 bytes x of this lane's row to dst (nullptr: none).
-template <bool STAGED>
-__device__ __forceinline__ void put64(uint32_t stg, const uint4 (&x)[4], void* dst) {
-  if constexpr (STAGED) {
-    stage_store(stg, x, dst);
-  } else if (dst) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) ((uint4*)dst)[j] = x[j];
+// One lane of a converged warp, and a wait that the warp agrees on.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity,
+                                          volatile int* abort_flag, int32_t* status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
+}
+
+// 32 bytes to dst: one store where it is aligned to them (whole sectors, so rows
+// go straight from the lanes that hold them), two otherwise.
+__device__ __forceinline__ void put32(void* dst, bool wide, uint32_t a, uint32_t b, uint32_t c,
+                                      uint32_t d, uint32_t e, uint32_t f, uint32_t g, uint32_t h) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a),
+                 "r"(b), "r"(c), "r"(d), "r"(e), "r"(f), "r"(g), "r"(h)
+                 : "memory");
+  } else {
+    ((uint4*)dst)[0] = make_uint4(a, b, c, d);
+    ((uint4*)dst)[1] = make_uint4(e, f, g, h);
   }
 }
 
 template <int R, int MT>
-__global__ void __launch_bounds__(32 * Cfg<R, MT>::WARPS, 1)
+__global__ void __launch_bounds__(kThreads, 1)
 cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmC,
-                  const CacheAttn p, const int min_quota) {
+                  const CacheAttn p) {
   using C = Cfg<R, MT>;
   using Line = ByRows<MT, KT>;
-  constexpr int KP = C::KP, RSUB = C::RSUB, KS = C::KS, OBUF = C::OBUF, QBUF = C::QBUF;
+  constexpr int RSUB = C::RSUB, KS = C::KS, OBUF = C::OBUF, QBUF = C::QBUF;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* sQ = smem;
   uint8_t* sKV = sQ + QBUF * C::Q_BYTES;
-  uint64_t* bars = (uint64_t*)(sKV + KS * C::KV_BYTES);
+  uint64_t* bars = (uint64_t*)(sKV + KS * C::H_BYTES);
   uint64_t* q_full = bars;                 // [2]
   uint64_t* q_empty = bars + 2;            // [2]
-  uint64_t* s_full = bars + 4;             // [2]
-  uint64_t* p_full = bars + 6;             // [2] every softmax warp has written P
-  uint64_t* p_empty = bars + 8;            // [2] P C done
-  uint64_t* o_full = bars + 10;            // [2] last P C done, sums and maxima written
-  uint64_t* o_free = bars + 12;            // [2] the epilogue has read O
-  uint64_t* pair_bar = bars + 14;          // [4] the two softmax warps of a lane quadrant
-  uint64_t* kv_full = bars + 18;           // [KS]
+  uint64_t* o_full = bars + 4;             // [2] last P C done, sums and maxima written
+  uint64_t* o_free = bars + 6;             // [2] the epilogue has read O
+  uint64_t* s_full = bars + 8;             // [2] by tile
+  uint64_t* p_full = bars + 12;            // [NG] every softmax warp of the group has written P
+  uint64_t* p_empty = bars + 16;           // [NG] P C done
+  uint64_t* m_full = bars + 20;            // [NG][4] a quadrant's maximum after a tile
+  uint64_t* kv_full = bars + 36;           // [KS]
   uint64_t* kv_empty = kv_full + KS;       // [KS]
   uint64_t* drain = kv_empty + KS;
-  uint32_t* tmem_slot = (uint32_t*)(drain + 1);
+  uint32_t* tmem_slot = (uint32_t*)(drain + 2);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   CacheSplit* split = (CacheSplit*)(tmem_slot + 2);
-  static_assert((18 + 2 * KS + 1) * 8 + 8 + sizeof(CacheSplit) <= C::BAR_BYTES, "barriers");
-  float* lbuf = (float*)((uint8_t*)bars + C::BAR_BYTES);     // [2][MT] row sums
-  float* mbuf = lbuf + 2 * MT;                               // [2][MT] row maxima
-  float* mx = mbuf + 2 * MT;                                 // [2][2][MT] partial maxima
-  uint8_t* sStage = (uint8_t*)(mx + 4 * MT);
+  static_assert((36 + 2 * KS + 2) * 8 + 8 + sizeof(CacheSplit) <= C::BAR_BYTES, "barriers");
+  // of every row: by O buffer and group a sum and its base, by group the maximum so far
+  float* lbuf = (float*)((uint8_t*)bars + C::BAR_BYTES);     // [OBUF][NG][MT]
+  float* mbuf = lbuf + OBUF * NG * MT;                       // [OBUF][NG][MT]
+  float* mrow = mbuf + OBUF * NG * MT;                       // [NG][MT]
 
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quad = warp & 3;
   const CacheCall& c = p.c;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&q_full[s], 1);
       mbar_init(&q_empty[s], 1);
+      mbar_init(&o_full[s], 1 + NG * C::NQ);
+      mbar_init(&o_free[s], C::NQ);
       mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[s], C::NSOFT);
+    }
+    for (int s = 0; s < NG; ++s) {
+      mbar_init(&p_full[s], C::NQ);
       mbar_init(&p_empty[s], 1);
-      mbar_init(&o_full[s], 1 + C::NSOFT);
-      mbar_init(&o_free[s], C::NEPI);
+      for (int q = 0; q < 4; ++q) mbar_init(&m_full[s * 4 + q], 1);
     }
     for (int s = 0; s < KS; ++s) { mbar_init(&kv_full[s], 1); mbar_init(&kv_empty[s], 1); }
-    for (int q = 0; q < 4; ++q) mbar_init(&pair_bar[q], 2);
     mbar_init(drain, 1);
+    mbar_init(drain + 1, 1);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmC);
   }
-  for (int i = threadIdx.x; i < 2 * MT; i += blockDim.x) lbuf[i] = 0.f;
-  if (warp == C::MMA) {
+  if (warp == 1) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
   // everything below reads what earlier kernels wrote
   pdl_wait();
-  cache_split<Line>(c, min_quota, (int32_t*)sKV, split);
+  cache_split<Line>(c, p.min_quota, p.never_cut, *(CacheSplitSpace*)sKV, split);
   fence_proxy_async_smem();               // the ring's next writes come from TMA
   tc_fence_before();
   __syncthreads();
@@ -169,33 +228,35 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   const uint32_t tmem = *tmem_slot;
   const CacheSplit run = *split;
 
-  if (warp == C::PROD) {
+  if (warp < 4) {
+  regs_down<kRegsIssue>();
+  if (warp == 0) {
     // ------------------------------------------------------------ producer
-    // Lane l < pages of a tile gathers page l; a page that no row of the block
-    // sees, or that is outside the pool, reads as zeros (a box past the pool's
-    // last row).
+    // Lane l < boxes of half a tile gathers box l, a page or, of a larger page, a part; events that no row of the block sees, and pages outside the pool, read
+    // as zeros (a box past the pool's last row).
     uint32_t itm = 0, g = 0, qi = 0;
-    const int32_t P = 1 << c.page_shift;
-    const int np = KT >> c.page_shift;
+    const int32_t P = min(1 << c.page_shift, kCacheBox);     // events of a box
+    const int np = HT / P;
     const int32_t outside = c.n_pages << c.page_shift;
     CacheItems<Line> items;
     items.start(c, run);
-    CacheItem it;
+    CacheItem<Line> it;
     bool ok = true;
     while (ok && items.next(c, it)) {
-      const CacheBlock blk = cache_block<MT, KT>(c, it.x, it.b);
+      const CacheBlock& blk = it.k;
       if (it.x.len == 0) continue;
       const int32_t* row = c.table + (int64_t)it.u * c.stride;
-      // pool row of this lane's page in tile i of the piece
-      auto place = [&](int i) -> int32_t {
-        const int32_t t = cache_tile(blk, i) * KT + lane * P;
+      // pool row of this lane's box in half h of the piece's tiles
+      auto place = [&](int h) -> int32_t {
+        const int32_t t = cache_tile(blk, h >> 1) * KT + (h & 1) * HT + lane * P;
         if (lane >= np || !cache_seen(c, blk, t, t + P)) return outside;
         const int32_t page = __ldg(row + (t >> c.page_shift));
-        if ((uint32_t)page < (uint32_t)c.n_pages) return page << c.page_shift;
+        if ((uint32_t)page < (uint32_t)c.n_pages)
+          return (page << c.page_shift) + (t & ((1 << c.page_shift) - 1));
         atomicOr(c.status, LLATTE_DEV_BAD_ID);
         return outside;
       };
-      int32_t y = place(it.t0);
+      int32_t y = place(2 * it.t0);
       const int qb = itm % QBUF;
       if (lane == 0) {
         ok = mbar_wait(&q_empty[qb], ((itm / QBUF) & 1) ^ 1, abort_flag, c.status);
@@ -210,17 +271,17 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
-      for (int i = it.t0; i < it.t1; ++i, ++g) {
-        const int32_t y_next = i + 1 < it.t1 ? place(i + 1) : 0;
+      for (int i = 2 * it.t0; i < 2 * it.t1; ++i, ++g) {
+        const int32_t y_next = i + 1 < 2 * it.t1 ? place(i + 1) : 0;
         const int st = g % KS;
         if (lane == 0) {
           ok = mbar_wait(&kv_empty[st], ((g / KS) & 1) ^ 1, abort_flag, c.status);
-          if (ok) mbar_arrive_expect_tx(&kv_full[st], C::KV_BYTES);
+          if (ok) mbar_arrive_expect_tx(&kv_full[st], C::H_BYTES);
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
         if (lane < np) {
-          uint8_t* dst = sKV + st * C::KV_BYTES + lane * P * 128;
+          uint8_t* dst = sKV + st * C::H_SUB + lane * P * 128;
 #pragma unroll
           for (int s = 0; s < RSUB; ++s)
             tma_load_2d(&tmC, &kv_full[st], dst + s * C::KV_SUB, s * 64, y);
@@ -236,268 +297,291 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       drain_ring(q_full, QBUF, qi, c.status);
     }
     __syncwarp();
-  } else if (warp == C::MMA) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t IDESC_S = idesc_bf16(128, KT, false, false);
-      constexpr uint32_t IDESC_O = idesc_bf16(128, R, false, true);
-      uint32_t itm = 0, g = 0;
-      bool ok = true;
-      // S(gg) into S buffer gg & 1, which last held P(gg - 2): its product was
-      // issued before this call and the tensor pipe works in order.
-      auto issue_s = [&](uint32_t gg, uint32_t q_addr) -> bool {
-        const int st = gg % KS;
-        if (!mbar_wait(&kv_full[st], (gg / KS) & 1, abort_flag, c.status)) return false;
-        tc_fence_after();
-        const uint32_t kv_addr = smem_u32(sKV + st * C::KV_BYTES);
-        const uint32_t d = tmem + C::S_COL + (gg & 1) * KT;
-#pragma unroll
-        for (int k = 0; k < R / 16; ++k) {
-          const uint64_t ad = sdesc_sw128(q_addr + (k >> 2) * C::QSUB + (k & 3) * 32, 16, 1024);
-          const uint64_t bd = sdesc_sw128(kv_addr + (k >> 2) * C::KV_SUB + (k & 3) * 32, 16, 1024);
-          umma_bf16(d, ad, bd, IDESC_S, k > 0 ? 1u : 0u);
-        }
-        umma_commit(&s_full[gg & 1]);
-        return true;
-      };
-      // O (+)= P(gg) C: P from TMEM, the tile read MN-major; `first` starts O anew.
-      auto issue_pv = [&](uint32_t gg, bool first, int ob, uint32_t item) -> bool {
-        if (!mbar_wait(&p_full[gg & 1], (gg >> 1) & 1, abort_flag, c.status)) return false;
-        if (first && !mbar_wait(&o_free[ob], ((item / OBUF) & 1) ^ 1, abort_flag, c.status))
-          return false;
-        tc_fence_after();
-        const int st = gg % KS;
-        const uint32_t kv_addr = smem_u32(sKV + st * C::KV_BYTES);
-        const uint32_t p_tmem = tmem + C::S_COL + (gg & 1) * KT;
-#pragma unroll
-        for (int k = 0; k < KT / 16; ++k) {
-          const uint64_t bd = sdesc_sw128(kv_addr + k * 2048, C::KV_SUB, 1024);
-          umma_bf16_ts(tmem + ob * R, p_tmem + p_col<KP>(k), bd, IDESC_O,
-                       (!first || k > 0) ? 1u : 0u);
-        }
-        umma_commit(&kv_empty[st]);
-        umma_commit(&p_empty[gg & 1]);
-        return true;
-      };
-      // The product of a tile is issued after the S of the next one, also across
-      // items, so that a tile's softmax overlaps the next S.
-      struct Pending { uint32_t g, item; int ob; bool first, last, valid; };
-      Pending pend = {0, 0, 0, false, false, false};
-      auto flush = [&]() -> bool {
-        if (!pend.valid) return true;
-        if (!issue_pv(pend.g, pend.first, pend.ob, pend.item)) return false;
-        if (pend.last) umma_commit(&o_full[pend.ob]);
-        pend.valid = false;
-        return true;
-      };
-      CacheItems<Line> items;
-      items.start(c, run);
-      CacheItem it;
-      while (ok && items.next(c, it)) {
-        if (it.x.len == 0) continue;
-        const int ob = itm % OBUF, qb = itm % QBUF;
-        if (QBUF == 1 && !flush()) break;
-        if (!mbar_wait(&q_full[qb], (itm / QBUF) & 1, abort_flag, c.status)) break;
-        const uint32_t q_addr = smem_u32(sQ + qb * C::Q_BYTES);
-        for (int i = it.t0; i < it.t1; ++i, ++g) {
-          if (!issue_s(g, q_addr)) { ok = false; break; }
-          if (i == it.t1 - 1) umma_commit(&q_empty[qb]);
-          if (!flush()) { ok = false; break; }
-          pend = {g, itm, ob, i == it.t0, i == it.t1 - 1, true};
-        }
-        ++itm;
-      }
-      if (ok) flush();
-      umma_commit(drain);
-      int dummy = 0;
-      mbar_wait(drain, 0, &dummy, c.status);
-    }
-    __syncwarp();
-  } else if (C::SMALL ? (warp == 0 || warp == 4) : (warp >= 2 && warp < 10)) {
-    // ------------------------------------------------------------ softmax
-    const int quad = warp & 3;
-    const int part = C::SMALL ? warp >> 2 : (warp - 2) >> 2;    // half of the tile's events
-    const int row = quad * 32 + lane;                  // pair in the block = TMEM lane
-    const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
-    const float mul = p.scale2 == 0.f ? 1.f : fabsf(p.scale2);
-    const float2 mul2 = make_float2(mul, mul);
-    uint32_t g = 0, itm = 0, pphase = 0;
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ S = Q C^T
+    // Two warps issue, so that neither a tile on its way from memory nor a softmax
+    // holds up the other's products.  Both stay converged and one lane issues:
+    // descriptors then live in uniform registers (from one divergent lane an MMA took
+    // 68 cycles to issue, more than it takes to run).
+    constexpr uint32_t IDESC_S = idesc_bf16(128, KT, false, false);
+    const bool elect = elect_one();
+    uint32_t itm = 0, g = 0;               // items, tiles
     bool ok = true;
     CacheItems<Line> items;
     items.start(c, run);
-    CacheItem it;
+    CacheItem<Line> it;
     while (ok && items.next(c, it)) {
-      const CacheBlock blk = cache_block<MT, KT>(c, it.x, it.b);
+      if (it.x.len == 0) continue;
+      const int qb = itm % QBUF;
+      if (!warp_wait(&q_full[qb], (itm / QBUF) & 1, abort_flag, c.status)) break;
+      const uint64_t ad = sdesc_sw128(smem_u32(sQ + qb * C::Q_BYTES), 16, 1024);
+      for (int i = it.t0; i < it.t1; ++i, ++g) {
+        const int st = (2 * g) % KS, sb = g & 1;
+        // both halves are here; the products that read P in this S buffer are done
+        ok = warp_wait(&kv_full[st], (2 * g / KS) & 1, abort_flag, c.status) &&
+             warp_wait(&kv_full[st + 1], (2 * g / KS) & 1, abort_flag, c.status) &&
+             warp_wait(&p_empty[2 * sb + 1], ((g >> 1) & 1) ^ 1, abort_flag, c.status);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t bd = sdesc_sw128(smem_u32(sKV + st * C::H_SUB), 16, 1024);
+        const uint32_t d = tmem + C::S_COL + sb * KT;
+        const bool last = i == it.t1 - 1;
+        if (elect) {
+#pragma unroll
+          for (int k = 0; k < R / 16; ++k)
+            umma_bf16(d, ad + (((k >> 2) * C::QSUB + (k & 3) * 32) >> 4),
+                      bd + (((k >> 2) * C::KV_SUB + (k & 3) * 32) >> 4), IDESC_S, k > 0 ? 1u : 0u);
+          umma_commit(&s_full[sb]);
+          if (last) umma_commit(&q_empty[qb]);
+        }
+        __syncwarp();
+      }
+      ++itm;
+    }
+    if (elect) umma_commit(drain);
+    __syncwarp();
+    int dummy = 0;
+    mbar_wait(drain, 0, &dummy, c.status);
+    __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ O += P C
+    // P from TMEM, half a tile read MN-major; the first half of an item starts O anew.
+    constexpr uint32_t IDESC_O = idesc_bf16(128, R, false, true);
+    const bool elect = elect_one();
+    uint32_t itm = 0, g = 0;               // items, halves
+    bool ok = true;
+    CacheItems<Line> items;
+    items.start(c, run);
+    CacheItem<Line> it;
+    while (ok && items.next(c, it)) {
       if (it.x.len == 0) continue;
       const int ob = itm % OBUF;
-      const uint32_t o_col = ob * R + part * (R / 2);          // this warp's half of O
+      if (!warp_wait(&o_free[ob], ((itm / OBUF) & 1) ^ 1, abort_flag, c.status)) break;
+      for (int i = 2 * it.t0; i < 2 * it.t1; ++i, ++g) {
+        const int st = g % KS, sb = g % NG;
+        ok = warp_wait(&p_full[sb], (g / NG) & 1, abort_flag, c.status);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t bd = sdesc_sw128(smem_u32(sKV + st * C::H_SUB), C::KV_SUB, 1024);
+        const uint32_t p_tmem = tmem + C::S_COL + sb * HT;
+        const bool first = i == 2 * it.t0, last = i == 2 * it.t1 - 1;
+        if (elect) {
+#pragma unroll
+          for (int k = 0; k < HT / 16; ++k)
+            umma_bf16_ts(tmem + ob * R, p_tmem + k * 8, bd + (k * 2048 >> 4), IDESC_O,
+                         (!first || k > 0) ? 1u : 0u);
+          umma_commit(&kv_empty[st]);
+          umma_commit(&p_empty[sb]);
+          if (last) umma_commit(&o_full[ob]);
+        }
+        __syncwarp();
+      }
+      ++itm;
+    }
+    if (elect) umma_commit(drain + 1);
+    __syncwarp();
+    int dummy = 0;
+    mbar_wait(drain + 1, 0, &dummy, c.status);
+    __syncwarp();
+  }
+  } else if (warp < 20) {
+  if (quad < C::NQ) {
+    // ------------------------------------------------------------ softmax
+    // The groups take the halves in turn, group g % NG half g with S buffer g % NG; a
+    // thread owns a row.  Only the running maximum goes from one group to the next,
+    // as soon as it is known, so that the latencies of NG halves overlap.
+    const int group = (warp >> 2) - 1, before = (group + NG - 1) % NG;
+    const int row = quad * 32 + lane;                  // pair in the block = TMEM lane
+    const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
+    const uint32_t s_addr = lane_base + C::S_COL + group * HT;
+    const float mul = p.scale2 == 0.f ? 1.f : fabsf(p.scale2);
+    const float2 mul2 = make_float2(mul, mul);
+    uint32_t g = 0, itm = 0;
+    bool ok = true;
+    CacheItems<Line> items;
+    items.start(c, run);
+    CacheItem<Line> it;
+    while (ok && items.next(c, it)) {
+      if (it.x.len == 0) continue;
+      const CacheBlock& blk = it.k;
+      const int ob = itm % OBUF;
       const uint32_t pairs = (uint32_t)it.x.n * (uint32_t)c.heads;
       const uint32_t pair = (uint32_t)it.b * MT + row;
       const bool valid = pair < pairs;
       const int32_t pos = valid ? cache_pos(it.x, (int)(pair / (uint32_t)c.heads)) : blk.pmax;
-      const int32_t low = cache_low(c, pos);
+      const int32_t low = cache_low(c, pos), low_max = cache_low(c, blk.pmax);
       const bool idle = (uint32_t)it.b * MT + quad * 32 >= pairs;   // no row in this quadrant
-      float m_run = -INFINITY, l_run = 0.f;     // running maximum (log2 units), partial sum
+      float m_run = -INFINITY, l_run = 0.f;     // maximum (log2 units) that the sum is over
       bool poison = false;
-      for (int i = it.t0; i < it.t1; ++i, ++g) {
-        bool w = mbar_wait(&s_full[g & 1], (g >> 1) & 1, abort_flag, c.status);
+      for (int i = 2 * it.t0; i < 2 * it.t1; ++i, ++g) {
+        if ((int)(g % NG) != group) continue;
+        bool w = mbar_wait(&s_full[group >> 1], (g / NG) & 1, abort_flag, c.status);
         if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
-        if (idle) {
-          if (lane == 0) mbar_arrive(&p_full[g & 1]);
-          continue;
-        }
         tc_fence_after();
-        const uint32_t s_addr = lane_base + C::S_COL + (g & 1) * KT + part * KP;
-        const int32_t tile0 = cache_tile(blk, i) * KT;
-        float v[KP];
-        tmem_ld64(s_addr, v);
-        if (p.scale2 <= 0.f) {
-          const float f = p.scale2 == 0.f ? 0.f : -1.f;
-#pragma unroll
-          for (int k = 0; k < KP; ++k) v[k] *= f;
-        }
-        // some row hides some event of the tile (the same answer in every warp)
-        if (blk.pmin < tile0 + KT - 1 || cache_low(c, blk.pmax) > tile0) {
-          const int64_t t0 = tile0 + part * KP;
-          uint64_t vis = bits_below((int64_t)pos + 1 - t0);
-          if (c.window > 0) vis &= ~bits_below(low - t0) | bits_below(c.n_sink - t0);
-          if (!valid) vis = ~0ull;
-          float2 z2 = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int k = 0; k < KP; k += 2)
-            z2 = fma_f2(make_float2(v[k], v[k + 1]), make_float2(0.f, 0.f), z2);
-          if (__any_sync(0xffffffffu, valid && !(z2.x + z2.y == 0.f))) {
-            // a score is not finite: clear this warp's latents that are not
-            uint8_t* kv = sKV + (g % KS) * C::KV_BYTES;
+        float mt = -INFINITY;
+        if (!idle) {
+          // some row hides some event of the half (the same answer in every warp)
+          const int32_t tile0 = cache_tile(blk, i >> 1) * KT + (i & 1) * HT;
+          const bool masked = blk.pmin < tile0 + HT - 1 || low_max > tile0;
+          bool clear = false;
 #pragma unroll 1
-            for (int k = part * KP + lane; k < (part + 1) * KP; k += 32) {
-              bool bad = false;
-              for (int s = 0; s < RSUB; ++s) {
-                const uint4* e = (const uint4*)(kv + s * C::KV_SUB + k * 128);
-                for (int j = 0; j < 8; ++j) {
-                  const uint4 x = e[j];
-                  for (uint32_t y : {x.x, x.y, x.z, x.w})
-                    bad |= (y & 0x7f80u) == 0x7f80u || (y & 0x7f800000u) == 0x7f800000u;
+          for (int h = 0; h < HT; h += 32) {
+            float v[32];
+            tmem_ld32(s_addr + h, v);
+            if (masked || p.scale2 <= 0.f) {
+              if (p.scale2 <= 0.f) {
+                const float f = p.scale2 == 0.f ? 0.f : -1.f;
+#pragma unroll
+                for (int k = 0; k < 32; ++k) v[k] *= f;
+              }
+              // events that the row sees: [0, hi) without [sk, lo)
+              const int32_t t0 = tile0 + h;
+              const int hi = max(min(pos + 1 - t0, 32), 0);
+              const int lo = min(max(low - t0, 0), 32);
+              const int sk = max(min(c.n_sink - t0, lo), 0);
+              uint32_t vis = hi == 0 ? 0u : 0xffffffffu >> (32 - hi);
+              if (sk < lo) vis &= ~((0xffffffffu >> (32 - lo)) & (0xffffffffu << sk));
+              float2 z2 = make_float2(0.f, 0.f);
+#pragma unroll
+              for (int k = 0; k < 32; k += 2)
+                z2 = fma_f2(make_float2(v[k], v[k + 1]), make_float2(0.f, 0.f), z2);
+              if (__any_sync(0xffffffffu, valid && !(z2.x + z2.y == 0.f))) {
+                clear = masked;                // a score is not finite
+                if (masked) {
+#pragma unroll
+                  for (int k = 0; k < 32; ++k) {
+                    const bool fin = fabsf(v[k]) < INFINITY;
+                    poison |= valid && !fin && ((vis >> k) & 1);
+                    v[k] = fin ? v[k] : -INFINITY;
+                  }
                 }
               }
-              if (!bad) continue;
-              for (int s = 0; s < RSUB; ++s)
-                for (int j = 0; j < 8; ++j)
-                  ((uint4*)(kv + s * C::KV_SUB + k * 128))[j] = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
+              if (masked) {
 #pragma unroll
-            for (int k = 0; k < KP; ++k) {
-              const bool fin = fabsf(v[k]) < INFINITY;
-              poison |= valid && !fin && ((vis >> k) & 1);
-              v[k] = fin ? v[k] : -INFINITY;
+                for (int k = 0; k < 32; ++k) v[k] = (vis >> k) & 1 ? v[k] : -INFINITY;
+              }
+              tmem_st32(s_addr + h, v);
             }
+            float m8[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) m8[k] = fmaxf(fmax3(v[k], v[k + 8], v[k + 16]), v[k + 24]);
+            mt = fmaxf(mt, fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]),
+                                 fmaxf(m8[6], m8[7])));
           }
-#pragma unroll
-          for (int k = 0; k < KP; ++k) v[k] = ((vis >> k) & 1) ? v[k] : -INFINITY;
+          if (clear) clear_rows<R>(sKV + (g % KS) * C::H_SUB, C::KV_SUB);
+          mt *= mul;
         }
-        float m8[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) m8[k] = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < KP; k += 16) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) m8[j] = fmax3(m8[j], v[k + j], v[k + 8 + j]);
+        // the maximum so far comes from the group before (a new block starts anew);
+        // waiting for it in every tile also says that mrow[group] has been read
+        if (g > 0) {
+          w = mbar_wait(&m_full[before * 4 + quad], ((g - 1) / NG) & 1, abort_flag, c.status);
+          if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
         }
-        float mt = mul * fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
-                               fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
-        // the two halves of the row meet: both warps end with the same maximum
-        float* mxs = mx + (g & 1) * 2 * MT;
-        mxs[part * MT + row] = mt;
-        if (!group_sync(&pair_bar[quad], pphase, abort_flag, c.status)) { ok = false; break; }
-        mt = fmaxf(mt, mxs[(part ^ 1) * MT + row]);
-        // O and l are rescaled only when the maximum grows by more than 2^8
-        float scale = 1.f;
-        bool resc = false;
-        if (i == it.t0) {
-          m_run = mt;
-        } else if (mt > m_run + 8.f) {
-          scale = ex2_approx(m_run - mt);
-          m_run = mt;
-          resc = true;
+        const float m_prev = i == 2 * it.t0 ? -INFINITY : mrow[before * MT + row];
+        // O and the sums keep their base until the maximum grows by more than 2^8
+        const bool resc = i > 2 * it.t0 && mt > m_prev + 8.f;
+        const float m_now = i == 2 * it.t0 || resc ? mt : m_prev;
+        mrow[group * MT + row] = m_now;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&m_full[group * 4 + quad]);
+        if (idle) {
+          if (lane == 0) mbar_arrive(&p_full[group]);
+          continue;
         }
         if (__any_sync(0xffffffffu, resc)) {
           // the previous product must be in O: the next phase of its p_empty
-          bool w2 = mbar_wait(&p_empty[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag, c.status);
-          if (!__all_sync(0xffffffffu, w2)) { ok = false; break; }
+          w = mbar_wait(&p_empty[before], ((g - 1) / NG) & 1, abort_flag, c.status);
+          if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
           tc_fence_after();
+          const float scale = resc ? ex2_approx(m_prev - m_now) : 1.f;
 #pragma unroll 1
-          for (int k = 0; k < R / 2; k += 32) {
+          for (int k = 0; k < R; k += 32) {
             float o[32];
-            tmem_ld32(lane_base + o_col + k, o);
+            tmem_ld32(lane_base + ob * R + k, o);
 #pragma unroll
             for (int j = 0; j < 32; ++j) o[j] *= scale;
-            tmem_st32(lane_base + o_col + k, o);
+            tmem_st32(lane_base + ob * R + k, o);
           }
-          l_run *= scale;
         }
         // weights 2^(s - m), the sum in fp32 of the unrounded ones; a row that has
-        // seen nothing yet subtracts 0 from its -inf
-        const float m_use = m_run > -INFINITY ? m_run : 0.f;
+        // seen nothing yet subtracts 0 from its -inf.  One pair in four takes the
+        // FMA pipe: the special-function unit's 4 exponentials a cycle and scheduler
+        // would cost a tile 512 cycles.
+        const float m_use = m_now > -INFINITY ? m_now : 0.f;
         const float2 nm2 = make_float2(-m_use, -m_use);
-        float2 l4[4];
+        float2 l4[2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) l4[k] = make_float2(0.f, 0.f);
-        float pk[KP / 2];                      // bf16 pairs
+        for (int k = 0; k < 2; ++k) l4[k] = make_float2(0.f, 0.f);
+#pragma unroll 1
+        for (int h = 0; h < HT; h += 32) {
+          float v[32];
+          tmem_ld32(s_addr + h, v);
+          uint32_t pk[16];                     // bf16 pairs
 #pragma unroll
-        for (int k = 0; k < KP / 2; ++k) {
-          float2 x = fma_f2(make_float2(v[2 * k], v[2 * k + 1]), mul2, nm2);
-          x.x = ex2_approx(x.x);
-          x.y = ex2_approx(x.y);
-          l4[k & 3] = add_f2(l4[k & 3], x);
-          pk[k] = __uint_as_float(pack_bf16(x.x, x.y));
+          for (int k = 0; k < 16; ++k) {
+            float2 x = fma_f2(make_float2(v[2 * k], v[2 * k + 1]), mul2, nm2);
+            if ((k & 3) == 3) {
+              x = exp2_fma(x);
+            } else {
+              x.x = ex2_approx(x.x);
+              x.y = ex2_approx(x.y);
+            }
+            l4[k & 1] = add_f2(l4[k & 1], x);
+            pk[k] = pack_bf16(x.x, x.y);
+          }
+          tmem_st16u(s_addr + h / 2, pk);      // over scores already read
         }
-        l_run += ((l4[0].x + l4[0].y) + (l4[1].x + l4[1].y)) +
-                 ((l4[2].x + l4[2].y) + (l4[3].x + l4[3].y));
-        tmem_st32(s_addr, pk);                 // waits for the store
+        tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[g & 1]);
+        if (lane == 0) mbar_arrive(&p_full[group]);
+        // the sum's base follows the maximum (also past changes of the other groups);
+        // -inf: no sum yet
+        if (m_now != m_run) {
+          l_run = m_run > -INFINITY ? l_run * ex2_approx(m_run - m_now) : 0.f;
+          m_run = m_now;
+        }
+        l_run += (l4[0].x + l4[0].y) + (l4[1].x + l4[1].y);
       }
       if (!ok) break;
-      bool w4 = mbar_wait(&o_free[ob], ((itm / OBUF) & 1) ^ 1, abort_flag, c.status);
-      if (!__all_sync(0xffffffffu, w4)) break;
+      const bool w_free = mbar_wait(&o_free[ob], ((itm / OBUF) & 1) ^ 1, abort_flag, c.status);
+      if (!__all_sync(0xffffffffu, w_free)) break;
       if (!idle) {
         if (poison || m_run == INFINITY) l_run = NAN;
-        atomicAdd(&lbuf[ob * MT + row], l_run);     // zero before the two halves' sums
-        if (part == 0) mbuf[ob * MT + row] = m_run;
+        lbuf[(ob * NG + group) * MT + row] = l_run;
+        mbuf[(ob * NG + group) * MT + row] = m_run;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&o_full[ob]);
       ++itm;
     }
-  } else if (warp >= C::EPI0) {
+  }
+  } else {
+  regs_up<kRegsEpi>();
+  if (quad < C::NQ) {
     // ------------------------------------------------------------ epilogue
-    const int quad = warp & 3;
     const int row = quad * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
-    const uint32_t stg = smem_u32(sStage + (warp - C::EPI0) * C::STAGE);
+    const bool wide = ((uintptr_t)p.out & 31) == 0;
     CacheJoin* join = p.join + blockIdx.x;
-    const bool writer = warp == C::EPI0 && lane == 0;
+    const bool writer = warp == 20 && lane == 0;
     if (writer) join->rows = 0;
     uint32_t itm = 0;
     CacheItems<Line> items;
     items.start(c, run);
-    CacheItem it;
+    CacheItem<Line> it;
     while (items.next(c, it)) {
       const uint32_t pairs = (uint32_t)it.x.n * (uint32_t)c.heads;
       const uint32_t pair = (uint32_t)it.b * MT + row;
       const bool valid = pair < pairs;
       const bool idle = (uint32_t)it.b * MT + quad * 32 >= pairs;
       const int64_t at = it.x.row0 * c.heads + pair;
-      __nv_bfloat16* orow = valid ? (__nv_bfloat16*)p.out + at * R : nullptr;
+      __nv_bfloat16* orow = (__nv_bfloat16*)p.out + at * R;
       if (it.x.len == 0) {                 // no event: zeros
-        if (idle) continue;
-        const uint4 z[4] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0),
-                            make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-        for (int k = 0; k < R; k += 32) put64<!C::SMALL>(stg, z, orow ? orow + k : nullptr);
-        if (valid && p.lse) p.lse[at] = -INFINITY;
-        if (valid && p.lse2) p.lse2[at] = -INFINITY;
+        if (!valid) continue;
+        for (int k = 0; k < R; k += 16) put32(orow + k, wide, 0, 0, 0, 0, 0, 0, 0, 0);
+        if (p.lse) p.lse[at] = -INFINITY;
+        if (p.lse2) p.lse2[at] = -INFINITY;
         continue;
       }
       const int ob = itm % OBUF;
@@ -505,21 +589,28 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       if (!__all_sync(0xffffffffu, w)) break;
       tc_fence_after();
       if (!idle) {
-        const float l = lbuf[ob * MT + row], m = mbuf[ob * MT + row];
-        lbuf[ob * MT + row] = 0.f;         // ready for the item that reuses this buffer
+        // the groups' sums, each over its own last maximum; the largest is O's
+        float m = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int j = 0; j < NG; ++j) m = fmaxf(m, mbuf[(ob * NG + j) * MT + row]);
+        const float m_use = m > -INFINITY ? m : 0.f;
+#pragma unroll
+        for (int j = 0; j < NG; ++j)
+          l = fmaf(lbuf[(ob * NG + j) * MT + row],
+                   ex2_approx(mbuf[(ob * NG + j) * MT + row] - m_use), l);
+        const uint32_t o_addr = lane_base + ob * R;
         if (it.whole) {
           const float inv = l != 0.f ? 1.f / l : 0.f;
 #pragma unroll 1
-          for (int k = 0; k < R; k += 64) {
-            float v[64];
-            tmem_ld64(lane_base + ob * R + k, v);
+          for (int k = 0; k < R; k += 32) {
+            float v[32];
+            tmem_ld32(o_addr + k, v);
+            uint32_t x[16];
 #pragma unroll
-            for (int j = 0; j < 64; ++j) v[j] *= inv;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint4 x[4];
-              pack_bf16x32(&v[32 * h], x);
-              put64<!C::SMALL>(stg, x, orow ? orow + k + 32 * h : nullptr);
+            for (int j = 0; j < 16; ++j) x[j] = pack_bf16(v[2 * j] * inv, v[2 * j + 1] * inv);
+            if (valid) {
+              put32(orow + k, wide, x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]);
+              put32(orow + k + 16, wide, x[8], x[9], x[10], x[11], x[12], x[13], x[14], x[15]);
             }
           }
           if (valid) {
@@ -530,21 +621,17 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         } else {
           // a part: O unnormalised, with its maximum and sum
           const int64_t slot = ((int64_t)blockIdx.x * 2 + (it.starts ? 1 : 0)) * MT + row;
-          float* prow = valid ? p.part_o + slot * R : nullptr;
+          float* prow = p.part_o + slot * R;
 #pragma unroll 1
-          for (int k = 0; k < R; k += 64) {
-            float v[64];
-            tmem_ld64(lane_base + ob * R + k, v);
+          for (int k = 0; k < R; k += 32) {
+            float v[32];
+            tmem_ld32(o_addr + k, v);
+            const uint32_t* x = (const uint32_t*)v;
+            if (valid) {
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              uint4 x[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                x[j] = make_uint4(__float_as_uint(v[16 * h + 4 * j]),
-                                  __float_as_uint(v[16 * h + 4 * j + 1]),
-                                  __float_as_uint(v[16 * h + 4 * j + 2]),
-                                  __float_as_uint(v[16 * h + 4 * j + 3]));
-              put64<!C::SMALL>(stg, x, prow ? prow + k + 16 * h : nullptr);
+              for (int j = 0; j < 32; j += 8)
+                put32(prow + k + j, true, x[j], x[j + 1], x[j + 2], x[j + 3], x[j + 4], x[j + 5],
+                      x[j + 6], x[j + 7]);
             }
           }
           if (valid) p.part_ml[slot] = make_float2(m, l);
@@ -561,8 +648,9 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       ++itm;
     }
   }
+  }
   __syncthreads();
-  if (warp == C::MMA) {
+  if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -631,25 +719,54 @@ cudaError_t launch_rm(const CacheAttn& a, const CUtensorMap& tmC, int num_sms, c
     cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<R, MT>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
     if (e != cudaSuccess) return e;
+    // the register split waits for what the launch does not have
+    cudaFuncAttributes f;
+    e = cudaFuncGetAttributes(&f, cache_attn_kernel<R, MT>);
+    if (e != cudaSuccess) return e;
+    if (f.numRegs * 6 < kRegsIssue + NG * kRegsSoft + kRegsEpi) return cudaErrorInvalidConfiguration;
     attr_devices |= 1ull << (dev & 63);
   }
   CUtensorMap tmQ;
   if (!make_tmap_bf16(&tmQ, a.q, (uint64_t)a.c.rows * a.c.heads, R, MT))
     return cudaErrorInvalidValue;
-  cudaError_t e = launch_dependent(cache_attn_kernel<R, MT>, dim3(num_sms), dim3(32 * C::WARPS),
-                                   C::SMEM, s, 1, tmQ, tmC, a, 1);
+  cudaError_t e = launch_dependent(cache_attn_kernel<R, MT>, dim3(num_sms), dim3(kThreads),
+                                   C::SMEM, s, 1, tmQ, tmC, a);
   if (e != cudaSuccess) return e;
-  return launch_dependent(cache_join_kernel<R>, dim3(num_sms, MT / 8), dim3(256), 0, s, 1, a, MT);
+  return a.never_cut ? cudaSuccess : launch_cache_join(a, MT, num_sms, s);
+}
+
+// Most tiles that a block of mt pairs reads, as far as the host can tell.
+int64_t most_tiles(const CacheCall& c, int mt) {
+  int64_t t = (c.cap + KT - 1) / KT;
+  if (c.window > 0)
+    t = std::min<int64_t>(t, ((int64_t)c.window + mt / c.heads + KT) / KT + 1 +
+                                 ((int64_t)c.n_sink + KT - 1) / KT);
+  return t;
 }
 
 template <int R>
-cudaError_t launch_r(const CacheAttn& a, const CUtensorMap& tmC, int num_sms, cudaStream_t s) {
-  // blocks of 32 pairs when a user has no more than that on average
-  if (a.c.rows * a.c.heads <= 32 * (int64_t)a.c.B) return launch_rm<R, 32>(a, tmC, num_sms, s);
+cudaError_t launch_r(CacheAttn a, const CUtensorMap& tmC, int num_sms, cudaStream_t s) {
+  // Blocks of up to 4 tiles are not cut: the tiles that a CTA may have too many of
+  // take less time than the launch that would join the parts.
+  a.min_quota = 1;
+  a.never_cut = most_tiles(a.c, 128) <= 4;
+  // few pairs a user on average: see cache_token_sm100.cu
+  if (a.c.rows * a.c.heads <= 16 * (int64_t)a.c.B) return launch_cache_token(a, tmC, num_sms, s);
+
   return launch_rm<R, 128>(a, tmC, num_sms, s);
 }
 
 }  // namespace
+
+cudaError_t launch_cache_join(const CacheAttn& a, int mt, int num_sms, cudaStream_t s) {
+  const dim3 grid(num_sms, mt / 8);
+  switch (a.c.r) {
+    case 64: return launch_dependent(cache_join_kernel<64>, grid, dim3(256), 0, s, 1, a, mt);
+    case 128: return launch_dependent(cache_join_kernel<128>, grid, dim3(256), 0, s, 1, a, mt);
+    case 256: return launch_dependent(cache_join_kernel<256>, grid, dim3(256), 0, s, 1, a, mt);
+    default: return cudaErrorInvalidValue;
+  }
+}
 
 bool cache_attn_tc_supported(int r) { return r == 64 || r == 128 || r == 256; }
 

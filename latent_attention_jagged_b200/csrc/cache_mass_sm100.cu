@@ -47,7 +47,7 @@ struct Cfg {
   static constexpr uint32_t TMEM_COLS = SB * NP;
   static_assert(SMEM <= 232448, "shared memory budget");
   static_assert(TMEM_COLS <= 512, "TMEM budget");
-  static_assert(KS * K_BYTES >= 4 * (LLATTE_CACHE_MAX_BATCH + 1), "prefix sums");
+  static_assert(KS * K_BYTES + QS * Q_BYTES >= sizeof(CacheSplitSpace), "split");
   static_assert(KS * K_BYTES + QS * Q_BYTES <= 229376, "rings");
 };
 
@@ -123,7 +123,7 @@ cache_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     tmem_relinquish();
   }
   pdl_wait();
-  cache_split<Line>(c, 1, (int32_t*)sK, split);
+  cache_split<Line>(c, 1, false, *(CacheSplitSpace*)sK, split);
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
@@ -134,22 +134,24 @@ cache_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     uint32_t kn = 0, qn = 0;               // tiles and blocks of pairs asked for
-    const int32_t P = 1 << c.page_shift;
-    const int np = KT >> c.page_shift;
+    const int32_t P = min(1 << c.page_shift, kCacheBox);     // events of a box
+    const int np = KT / P;
     const int32_t outside = c.n_pages << c.page_shift;
     CacheItems<Line> items;
     items.start(c, run);
-    CacheItem it;
+    CacheItem<Line> it;
     bool ok = true;
     while (ok && items.next(c, it)) {
-      const CacheBlock all = cache_all<KT>(c, it.x);
-      const int32_t tile = cache_tile(all, it.b);
+      const CacheBlock& all = it.k.all;
+      const int32_t tile = it.k.tile;
       int32_t y = outside;
       const int32_t t = tile * KT + lane * P;
       if (lane < np && cache_seen(c, all, t, t + P)) {
         const int32_t page = __ldg(c.table + (int64_t)it.u * c.stride + (t >> c.page_shift));
-        if ((uint32_t)page < (uint32_t)c.n_pages) y = page << c.page_shift;
-        else atomicOr(c.status, LLATTE_DEV_BAD_ID);
+        if ((uint32_t)page < (uint32_t)c.n_pages)
+          y = (page << c.page_shift) + (t & ((1 << c.page_shift) - 1));
+        else
+          atomicOr(c.status, LLATTE_DEV_BAD_ID);
       }
       const int ks = kn % KS;
       if (lane == 0) {
@@ -166,7 +168,6 @@ cache_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       }
       ++kn;
       if (lane == 0) {
-        const int b0 = Line::range(c, it.x, tile).x;
         for (int i = it.t0; i < it.t1; ++i, ++qn) {
           const int qs = qn % QS;
           if (!mbar_wait(&q_empty[qs], ((qn / QS) & 1) ^ 1, abort_flag, c.status)) {
@@ -174,7 +175,7 @@ cache_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             break;
           }
           mbar_arrive_expect_tx(&q_full[qs], C::Q_BYTES);
-          const int32_t qrow = (int32_t)(it.x.row0 * c.heads + (int64_t)(b0 + i) * NP);
+          const int32_t qrow = (int32_t)(it.x.row0 * c.heads + (int64_t)(it.k.first + i) * NP);
 #pragma unroll
           for (int s = 0; s < RSUB; ++s)
             tma_load_2d(&tmQ, &q_full[qs], sQ + qs * C::Q_BYTES + s * C::QSUB, s * 64, qrow);
@@ -196,7 +197,7 @@ cache_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       bool ok = true;
       CacheItems<Line> items;
       items.start(c, run);
-      CacheItem it;
+      CacheItem<Line> it;
       while (ok && items.next(c, it)) {
         const int ks = kn % KS;
         if (!mbar_wait(&k_full[ks], (kn / KS) & 1, abort_flag, c.status)) break;
@@ -240,18 +241,17 @@ cache_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     bool ok = true;
     CacheItems<Line> items;
     items.start(c, run);
-    CacheItem it;
+    CacheItem<Line> it;
     while (ok && items.next(c, it)) {
-      const CacheBlock all = cache_all<KT>(c, it.x);
-      const int32_t tile0 = cache_tile(all, it.b) * KT;
+      const CacheBlock& all = it.k.all;
+      const int32_t tile0 = it.k.tile * KT;
       const int32_t t = tile0 + quad * 32 + lane;          // this lane's event
       const uint32_t pairs = (uint32_t)it.x.n * (uint32_t)c.heads;
-      const int b0 = Line::range(c, it.x, tile0 / KT).x;
       float sum = 0.f;
       for (int i = it.t0; i < it.t1; ++i, ++qn) {
         const int sb = qn % SB;
         // this warp's pairs: log sums and positions, one or two a lane
-        const uint32_t pair0 = (uint32_t)(b0 + i) * NP + part * CP;
+        const uint32_t pair0 = (uint32_t)(it.k.first + i) * NP + part * CP;
         __syncwarp();
 #pragma unroll
         for (int k = lane; k < CP; k += 32) {

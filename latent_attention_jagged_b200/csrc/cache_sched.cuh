@@ -54,12 +54,14 @@ __device__ __forceinline__ bool cache_seen(const CacheCall& c, const CacheBlock&
 // each of its tiles, or one when it has none (its rows still get their zeros).
 template <int MT, int KT>
 struct ByRows {
+  using Block = CacheBlock;
   __device__ __forceinline__ static int blocks(const CacheCall& c, const CacheUser& x) {
     return (int)(((uint32_t)x.n * (uint32_t)c.heads + (MT - 1)) / MT);
   }
-  __device__ __forceinline__ static int32_t places(const CacheCall& c, const CacheUser& x, int b) {
-    return max(1, cache_block<MT, KT>(c, x, b).tiles);
+  __device__ __forceinline__ static Block block(const CacheCall& c, const CacheUser& x, int b) {
+    return cache_block<MT, KT>(c, x, b);
   }
+  __device__ __forceinline__ static int32_t places(const Block& k) { return max(1, k.tiles); }
 };
 
 // The events that any row of a user reads, as one block.
@@ -78,64 +80,85 @@ __device__ __forceinline__ CacheBlock cache_all(const CacheCall& c, const CacheU
 
 // The line of the accumulation kernel: blocks are a user's tiles of KT events; a
 // block takes a place for each block of NP pairs with a row that sees the tile.
+struct CacheTile {
+  CacheBlock all;              // what the user's rows read
+  int32_t tile;
+  int32_t first, last;         // blocks of pairs that see the tile
+};
+
 template <int NP, int KT>
 struct ByTiles {
+  using Block = CacheTile;
   __device__ __forceinline__ static int blocks(const CacheCall& c, const CacheUser& x) {
     return cache_all<KT>(c, x).tiles;
   }
-  // First and last block of pairs that sees tile `tile`.  The rows that see it lie
-  // between the first one at or after its start and the last one whose window
-  // reaches back to its end.
-  __device__ __forceinline__ static int2 range(const CacheCall& c, const CacheUser& x,
-                                               int32_t tile) {
-    const int64_t t0 = (int64_t)tile * KT, start = x.len - x.m;
+  // The rows that see a tile lie between the first one at or after its start and
+  // the last one whose window reaches back to its end.
+  __device__ __forceinline__ static Block block(const CacheCall& c, const CacheUser& x, int b) {
+    Block k;
+    k.all = cache_all<KT>(c, x);
+    k.tile = cache_tile(k.all, b);
+    const int64_t t0 = (int64_t)k.tile * KT, start = x.len - x.m;
     int64_t lo = max((int64_t)0, t0 - start), hi = x.n - 1;
     const int64_t last = t0 + KT - 2 + c.window;       // last position that sees its end
     if (c.window > 0 && t0 >= c.n_sink && x.len - 1 > last) hi = last - start;
-    return make_int2((int)((uint32_t)lo * (uint32_t)c.heads / NP),
-                     (int)(((uint32_t)hi * (uint32_t)c.heads + c.heads - 1) / NP));
+    k.first = (int)((uint32_t)lo * (uint32_t)c.heads / NP);
+    k.last = (int)(((uint32_t)hi * (uint32_t)c.heads + c.heads - 1) / NP);
+    return k;
   }
-  __device__ __forceinline__ static int32_t places(const CacheCall& c, const CacheUser& x, int b) {
-    const int2 r = range(c, x, cache_tile(cache_all<KT>(c, x), b));
-    return r.y - r.x + 1;
-  }
+  __device__ __forceinline__ static int32_t places(const Block& k) { return k.last - k.first + 1; }
 };
 
 // Where a CTA's run of places lies.
 struct CacheSplit {
   int32_t begin, end, quota;   // this CTA's run of places
   int32_t u, b, t;             // where it starts: user, block, place in the block
+  CacheUser x;                 // that user
 };
 
-// The cut at place `at` of `base` (a whole warp calls this): user, block and place
-// in the block.  A cut inside a block that is short against a CTA's run moves to
-// the nearer end of the block: the imbalance is at most an eighth of a run, and
-// the block need not be summed from parts.
+// Shared memory that a split works in: places before every user, and the users.
+struct CacheSplitSpace {
+  int32_t prefix[LLATTE_CACHE_MAX_BATCH + 4];
+  int2 user[LLATTE_CACHE_MAX_BATCH];        // rows, cached events
+};
+
+// The cut at place `at` of `base` (a whole warp calls this): where it lies and the
+// user there.  A cut inside a block that is short against a CTA's run moves to the
+// nearer end of the block: the imbalance is at most an eighth of a run, and the
+// block need not be summed from parts.  With `never` every cut moves.
 template <class W>
-__device__ __forceinline__ void cache_cut(const CacheCall& c, const int32_t* prefix, int64_t at,
-                                          int64_t base, int32_t quota, CacheSplit* s) {
+__device__ __forceinline__ void cache_cut(const CacheCall& c, const CacheSplitSpace& w, int64_t at,
+                                          int64_t base, int32_t quota, bool never,
+                                          CacheSplit* s) {
   const int lane = threadIdx.x & 31;
-  s->begin = s->end = (int32_t)at;
+  s->begin = (int32_t)at;
   s->u = c.B; s->b = s->t = 0;
+  s->x = {0, 0, 0, 0};
   if (at >= base) return;
-  // the last user whose places start at or before the cut (skips empty users)
-  int lo = 0, hi = c.B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (prefix[mid] <= at) lo = mid; else hi = mid - 1;
+  // the last user whose places start at or before the cut (skips empty users): a
+  // 32-way search
+  int lo = 0, n = c.B;                      // it is one of n users from lo
+  while (n > 1) {
+    const int step = (n + 31) / 32, i = lo + lane * step;
+    const uint32_t le = __ballot_sync(0xffffffffu, lane * step < n && w.prefix[min(i, c.B)] <= at);
+    const int k = 31 - __clz(le);           // lane 0 always answers yes
+    n = min(step, n - k * step);
+    lo += k * step;
   }
   s->u = lo;
-  const CacheUser x = cache_user(c, lo);
+  const int2 d = w.user[lo];
+  const CacheUser x = {0, d.x, max(0, d.x - c.n_cand), d.y};
+  s->x = x;
   const int nb = W::blocks(c, x);
-  int32_t left = (int32_t)at - prefix[lo];
+  int32_t left = (int32_t)at - w.prefix[lo];
   for (int b0 = 0; b0 < nb; b0 += 32) {
     const int b = b0 + lane;
-    const int32_t own = b < nb ? W::places(c, x, b) : 0;
+    const int32_t own = b < nb ? W::places(W::block(c, x, b)) : 0;
     int32_t v = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int32_t w = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += w;
+      const int32_t y = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += y;
     }
     const uint32_t in = __ballot_sync(0xffffffffu, b < nb && v > left);
     if (in) {
@@ -143,7 +166,7 @@ __device__ __forceinline__ void cache_cut(const CacheCall& c, const int32_t* pre
       const int32_t places = __shfl_sync(0xffffffffu, own, l);
       s->b = b0 + l;
       s->t = left - __shfl_sync(0xffffffffu, v - own, l);
-      if (s->t > 0 && places <= quota / 4) {
+      if (s->t > 0 && (never || places <= quota / 4)) {
         if (2 * s->t < places) {
           s->begin -= s->t;
         } else {
@@ -158,77 +181,92 @@ __device__ __forceinline__ void cache_cut(const CacheCall& c, const int32_t* pre
   }
 }
 
-// Every thread of the CTA calls this (it synchronises); prefix has B + 1 entries
-// of shared memory, prefix[u] = places before user u.  A call of 2^31 places or
-// more gets no work and LLATTE_DEV_TOO_LONG.
+// Every thread of the CTA calls this (it synchronises).  A run has min_quota places
+// or more.  A call of 2^31 places or more gets no work and LLATTE_DEV_TOO_LONG.
 template <class W>
-__device__ __forceinline__ void cache_split(const CacheCall& c, int min_quota, int32_t* prefix,
-                                            CacheSplit* out) {
+__device__ __forceinline__ void cache_split(const CacheCall& c, int min_quota, bool never,
+                                            CacheSplitSpace& w, CacheSplit* out) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   constexpr int64_t kTop = (int64_t)1 << 31;
-  int64_t mine = 0;                       // places this warp has found (all lanes)
-  for (int u0 = warp * 32; u0 < c.B; u0 += warps * 32) {
-    const int u = u0 + lane;
-    CacheUser x = {0, 0, 0, 0};
-    if (u < c.B) x = cache_user(c, u);
+  bool many = false, too_many = false;
+  for (int u = threadIdx.x; u < c.B; u += blockDim.x) {
+    const CacheUser x = cache_user(c, u);
     const int nb = W::blocks(c, x);
     int64_t places = 0;
-    if (nb <= 4)
-      for (int b = 0; b < nb; ++b) places += W::places(c, x, b);
-    // users of many blocks: the whole warp, one block per lane
-    for (uint32_t big = __ballot_sync(0xffffffffu, nb > 4); big; big &= big - 1) {
-      const int l = __ffs(big) - 1;
-      CacheUser y;
-      y.row0 = 0;
-      y.n = __shfl_sync(0xffffffffu, x.n, l);
-      y.m = __shfl_sync(0xffffffffu, x.m, l);
-      y.len = __shfl_sync(0xffffffffu, x.len, l);
-      const int nby = __shfl_sync(0xffffffffu, nb, l);
+    if (nb <= 4) {
+      for (int b = 0; b < nb; ++b) places += W::places(W::block(c, x, b));
+    } else {
+      many = true;
+      places = -1;
+    }
+    w.user[u] = make_int2(x.n, x.len);
+    w.prefix[u + 1] = (int32_t)min(places, kTop - 1);
+  }
+  // users of many blocks: a warp each, a block per lane
+  if (__syncthreads_or(many)) {
+    for (int u = warp; u < c.B; u += warps) {
+      if (w.prefix[u + 1] >= 0) continue;
+      const int2 d = w.user[u];
+      const CacheUser x = {0, d.x, max(0, d.x - c.n_cand), d.y};
+      const int nb = W::blocks(c, x);
       int64_t sum = 0;
-      for (int b = lane; b < nby; b += 32) sum += W::places(c, y, b);
+      for (int b = lane; b < nb; b += 32) sum += W::places(W::block(c, x, b));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (lane == l) places = sum;
+      too_many |= sum >= kTop;
+      __syncwarp();
+      if (lane == 0) w.prefix[u + 1] = (int32_t)min(sum, kTop - 1);
     }
-    mine += places;
-    if (u < c.B) prefix[u + 1] = (int32_t)min(places, kTop - 1);
+    too_many = __syncthreads_or(too_many);
   }
-  const int too_many = __syncthreads_or(mine >= kTop);
-  if (warp == 0) {
-    int64_t base = 0;
-    for (int u0 = 0; u0 < c.B; u0 += 32) {
-      const int u = u0 + lane;
-      int64_t v = u < c.B ? prefix[u + 1] : 0;
+  // warps 0 and 1 sum up the users, 32 runs of them, and find the CTA's two cuts
+  if (warp < 2) {
+    const int per = (c.B + 31) / 32, u0 = min(lane * per, c.B), u1 = min(u0 + per, c.B);
+    int64_t v = 0;
+    for (int u = u0; u < u1; ++u) v += w.prefix[u + 1];
+    int64_t incl = v;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t w = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += w;
-      }
-      if (u < c.B) prefix[u + 1] = (int32_t)min(base + v, kTop - 1);
-      base += __shfl_sync(0xffffffffu, v, 31);
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
     }
-    if (lane == 0) prefix[0] = 0;
-    __syncwarp();
+    int64_t base = __shfl_sync(0xffffffffu, incl, 31);
     if (too_many || base >= kTop) {
-      if (lane == 0) atomicOr(c.status, LLATTE_DEV_TOO_LONG);
+      if (lane == 0 && warp == 0) atomicOr(c.status, LLATTE_DEV_TOO_LONG);
       base = 0;
     }
-    CacheSplit s, e;
-    s.quota = (int32_t)max((int64_t)min_quota, (base + gridDim.x - 1) / gridDim.x);
-    const int64_t first = (int64_t)blockIdx.x * s.quota;
-    cache_cut<W>(c, prefix, min(first, base), base, s.quota, &s);
-    e.quota = s.quota;
-    cache_cut<W>(c, prefix, min(first + s.quota, base), base, s.quota, &e);
-    s.end = e.begin;
-    if (lane == 0) *out = s;
+    asm volatile("bar.sync 1, 64;" ::: "memory");       // both have read the places
+    if (warp == 0) {
+      int64_t sum = incl - v;
+      for (int u = u0; u < u1; ++u) {
+        sum += w.prefix[u + 1];
+        w.prefix[u + 1] = (int32_t)min(sum, kTop - 1);
+      }
+      if (lane == 0) w.prefix[0] = 0;
+    }
+    asm volatile("bar.sync 1, 64;" ::: "memory");
+    const int32_t quota = (int32_t)max((int64_t)min_quota, (base + gridDim.x - 1) / gridDim.x);
+    const int64_t at = (int64_t)(blockIdx.x + warp) * quota;
+    CacheSplit s;
+    cache_cut<W>(c, w, min(at, base), base, quota, never, &s);
+    if (lane == 0) {
+      if (warp == 0) {
+        out->begin = s.begin; out->quota = quota;
+        out->u = s.u; out->b = s.b; out->t = s.t; out->x = s.x;
+      } else {
+        out->end = s.begin;
+      }
+    }
   }
   __syncthreads();
 }
 
 // One piece of work: places [t0, t1) of block b of user u.
+template <class W>
 struct CacheItem {
   int32_t u, b;
   CacheUser x;
+  typename W::Block k;
   int32_t t0, t1;
   bool whole;                  // the block is not cut
   bool starts;                 // it starts in this CTA
@@ -258,13 +296,13 @@ struct CacheItems {
     pos = s.begin; end = s.end; quota = s.quota; u = s.u; b = s.b; t = s.t;
     nb = 0;
     if (pos < end) {
-      fetch(c, u);
-      x = cache_user_of(c, next_a, next_b, next_len);
+      x = s.x;
+      x.row0 = c.qoff[u];
       nb = W::blocks(c, x);
       fetch(c, u + 1);
     }
   }
-  __device__ __forceinline__ bool next(const CacheCall& c, CacheItem& it) {
+  __device__ __forceinline__ bool next(const CacheCall& c, CacheItem<W>& it) {
     if (pos >= end) return false;
     while (b >= nb) {                       // on to the next user with rows
       ++u;
@@ -275,7 +313,8 @@ struct CacheItems {
       fetch(c, u + 1);
     }
     it.u = u; it.b = b; it.x = x;
-    const int32_t places = W::places(c, x, b);
+    it.k = W::block(c, x, b);
+    const int32_t places = W::places(it.k);
     it.t0 = t;
     it.t1 = min(places, t + (end - pos));
     const int32_t g0 = pos - t;             // the block's first place in the line

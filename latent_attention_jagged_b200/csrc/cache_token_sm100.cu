@@ -1,0 +1,451 @@
+// Attention of few new rows over the paged latent cache (bf16, rank 64, 128 or 256):
+// the form for single tokens.
+//
+// With 16 (query row, head) pairs or fewer the work is bound by reading the cache: 4 r
+// flops per pair and event against 2 r bytes.  The 128-row tensor-memory products of
+// cache_attn_sm100.cu would run on padding, and every tile would wait for the chain
+// S -> softmax -> P C; here the warps do not wait for one another at all.  A block of
+// 16 pairs is one m16 operand; of a tile of 128 events each of 8 warps takes 16, with
+// its own running maximum, sum and 16 x r result in registers (mma.sync, scores and
+// weights never leave them), and the 8 results meet once per item.  A ninth warp keeps
+// 192 KB of tiles on their way.
+//
+// Measured against blocks of 32 pairs on tcgen05 (64 users, 2000 to 8000 events, 8 heads,
+// rank 256): 45 us there.
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "cache.h"
+#include "cache_call.cuh"
+#include "cache_sched.cuh"
+#include "tc_common.cuh"
+#include "tc_drain.cuh"
+
+namespace llatte {
+
+using namespace tc;
+
+namespace {
+
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int MT = 16;                    // pairs of a block
+constexpr int KT = 128;                   // events of a tile
+constexpr int NW = 8;                     // consumer warps, 16 events of a tile each
+// Three warpgroups, the third for the producer: the launch's 168 registers a thread
+// are dealt out again, 128 threads x (232 + 232 + 40) = 384 x 168.
+constexpr int kThreads = 384;
+constexpr int kRegsConsume = 232, kRegsProduce = 40;
+static_assert(2 * kRegsConsume + kRegsProduce <= 504, "registers of the launch");
+
+template <int R>
+struct Cfg {
+  static constexpr int RSUB = R / 64;
+  static constexpr int KS = 768 / R;                   // 192 KB of tiles
+  static constexpr uint32_t KV_SUB = KT * 128;
+  static constexpr uint32_t KV_BYTES = RSUB * KV_SUB;
+  static constexpr uint32_t MEET = NW * MT * 64 * 4;   // 64 columns of every warp's result
+  static constexpr uint32_t BAR_BYTES = 512;
+  static constexpr size_t SMEM = 1024 + KS * KV_BYTES + MEET + BAR_BYTES + 2 * NW * MT * 4;
+  static_assert(SMEM <= 232448, "shared memory budget");
+  static_assert(KS * KV_BYTES >= sizeof(CacheSplitSpace), "split");
+};
+
+// The consumer warps meet.
+__device__ __forceinline__ void meet_sync() {
+  asm volatile("bar.sync 2, %0;" ::"n"(32 * NW) : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The warp clears the latents of its 16 events that are not finite.
+template <int R>
+__device__ __forceinline__ void clear_rows(uint8_t* kv, int first) {
+  const int lane = threadIdx.x & 31, k = first + (lane & 15);
+  bool bad = false;
+  for (int s = lane >> 4; s < R / 64; s += 2) {
+    const uint4* e = (const uint4*)(kv + s * (KT * 128) + k * 128);
+    for (int j = 0; j < 8; ++j) {
+      const uint4 x = e[j];
+      for (uint32_t y : {x.x, x.y, x.z, x.w})
+        bad |= (y & 0x7f80u) == 0x7f80u || (y & 0x7f800000u) == 0x7f800000u;
+    }
+  }
+  bad |= __shfl_xor_sync(0xffffffffu, (int)bad, 16) != 0;
+  if (bad) {
+    for (int s = lane >> 4; s < R / 64; s += 2)
+      for (int j = 0; j < 8; ++j)
+        ((uint4*)(kv + s * (KT * 128) + k * 128))[j] = make_uint4(0, 0, 0, 0);
+  }
+  fence_proxy_async_smem();               // the slot's next writes come from TMA
+  __syncwarp();
+}
+
+template <int R>
+__global__ void __launch_bounds__(kThreads, 1)
+cache_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn p) {
+  using C = Cfg<R>;
+  using Line = ByRows<MT, KT>;
+  constexpr int RSUB = C::RSUB, KS = C::KS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* sKV = smem;
+  float* meet = (float*)(sKV + KS * C::KV_BYTES);          // [NW][MT][64]
+  uint64_t* bars = (uint64_t*)((uint8_t*)meet + C::MEET);
+  uint64_t* kv_full = bars;                // [KS]
+  uint64_t* kv_empty = kv_full + KS;       // [KS]
+  volatile int* abort_flag = (volatile int*)(kv_empty + KS);
+  CacheSplit* split = (CacheSplit*)(kv_empty + KS + 1);
+  static_assert((2 * KS + 2) * 8 + sizeof(CacheSplit) <= C::BAR_BYTES, "barriers");
+  float* sm_m = (float*)((uint8_t*)bars + C::BAR_BYTES);   // [NW][MT]
+  float* sm_l = sm_m + NW * MT;
+
+  pdl_trigger();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const CacheCall& c = p.c;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < KS; ++s) { mbar_init(&kv_full[s], 1); mbar_init(&kv_empty[s], NW); }
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmC);
+  }
+  pdl_wait();
+  cache_split<Line>(c, p.min_quota, p.never_cut, *(CacheSplitSpace*)sKV, split);
+  fence_proxy_async_smem();               // the ring's next writes come from TMA
+  __syncthreads();
+  const CacheSplit run = *split;
+
+  if (warp >= NW) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsProduce));
+    if (warp == NW) {
+    CacheItems<Line> items;
+    items.start(c, run);
+    CacheItem<Line> it;
+    // ------------------------------------------------------------ producer
+    // Lane l < boxes of a tile gathers box l (as in cache_attn_sm100.cu).
+    uint32_t g = 0;
+    const int32_t P = min(1 << c.page_shift, kCacheBox);
+    const int np = KT / P;
+    const int32_t outside = c.n_pages << c.page_shift;
+    bool ok = true;
+    while (ok && items.next(c, it)) {
+      if (it.x.len == 0) continue;
+      const int32_t* row = c.table + (int64_t)it.u * c.stride;
+      auto place = [&](int i) -> int32_t {
+        const int32_t t = cache_tile(it.k, i) * KT + lane * P;
+        if (lane >= np || !cache_seen(c, it.k, t, t + P)) return outside;
+        const int32_t page = __ldg(row + (t >> c.page_shift));
+        if ((uint32_t)page < (uint32_t)c.n_pages)
+          return (page << c.page_shift) + (t & ((1 << c.page_shift) - 1));
+        atomicOr(c.status, LLATTE_DEV_BAD_ID);
+        return outside;
+      };
+      int32_t y = place(it.t0);
+      for (int i = it.t0; i < it.t1; ++i, ++g) {
+        const int32_t y_next = i + 1 < it.t1 ? place(i + 1) : 0;
+        const int st = g % KS;
+        if (lane == 0) {
+          ok = mbar_wait(&kv_empty[st], ((g / KS) & 1) ^ 1, abort_flag, c.status);
+          if (ok) mbar_arrive_expect_tx(&kv_full[st], C::KV_BYTES);
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        if (lane < np) {
+          uint8_t* dst = sKV + st * C::KV_BYTES + lane * P * 128;
+#pragma unroll
+          for (int s = 0; s < RSUB; ++s)
+            tma_load_2d(&tmC, &kv_full[st], dst + s * C::KV_SUB, s * 64, y);
+        }
+        y = y_next;
+      }
+    }
+    __syncwarp();
+    if (lane == 0 && *abort_flag) drain_ring(kv_full, KS, g, c.status);
+    __syncwarp();
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsConsume));
+    CacheItems<Line> items;
+    items.start(c, run);
+    CacheItem<Line> it;
+    // ------------------------------------------------------------ consumers
+    const int grp = lane >> 2, t4 = lane & 3;          // row (and row + 8), column pair
+    CacheJoin* join = p.join + blockIdx.x;
+    if (threadIdx.x == 0) join->rows = 0;
+    uint32_t g = 0;
+    bool ok = true;
+    // ldmatrix rows of this lane: events 8 * (lane / 16) + lane % 8 for S, and
+    // 8 * (lane / 8 % 2) + lane % 8 for P C; 16-byte chunks are XORed with event % 8
+    const uint32_t k_row = (warp * 16 + ((lane >> 4) << 3) + (lane & 7)) * 128;
+    const uint32_t v_row = (warp * 16 + (((lane >> 3) & 1) << 3) + (lane & 7)) * 128;
+    const uint32_t k_chunk = (lane >> 3) & 1, v_chunk = lane >> 4, xr = lane & 7;
+    while (items.next(c, it)) {
+      const int64_t pair0 = (int64_t)it.b * MT;
+      const int32_t rows = (int32_t)min((int64_t)MT, (int64_t)it.x.n * c.heads - pair0);
+      const int64_t at0 = it.x.row0 * c.heads + pair0;
+      if (it.x.len == 0) {                 // no event: zeros
+        for (int i = threadIdx.x; i < rows * (R / 8); i += 32 * NW)
+          ((uint4*)((__nv_bfloat16*)p.out + at0 * R))[i] = make_uint4(0, 0, 0, 0);
+        for (int i = threadIdx.x; i < rows; i += 32 * NW) {
+          if (p.lse) p.lse[at0 + i] = -INFINITY;
+          if (p.lse2) p.lse2[at0 + i] = -INFINITY;
+        }
+        continue;
+      }
+      // the block's queries as A operands: rows grp and grp + 8 (zeros past the last)
+      uint32_t qa[R / 16][4];
+#pragma unroll
+      for (int k = 0; k < R / 16; ++k) {
+        const uint32_t* q0 = (const uint32_t*)((const __nv_bfloat16*)p.q + (at0 + grp) * R) + k * 8 + t4;
+        const uint32_t* q1 = q0 + 8 * (R / 2);
+        qa[k][0] = grp < rows ? __ldg(q0) : 0u;
+        qa[k][1] = grp + 8 < rows ? __ldg(q1) : 0u;
+        qa[k][2] = grp < rows ? __ldg(q0 + 4) : 0u;
+        qa[k][3] = grp + 8 < rows ? __ldg(q1 + 4) : 0u;
+      }
+      int32_t pos[2], low[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int32_t r = min(grp + 8 * h, rows - 1);
+        pos[h] = cache_pos(it.x, (int)((uint32_t)(pair0 + r) / (uint32_t)c.heads));
+        low[h] = cache_low(c, pos[h]);
+      }
+      const int32_t low_max = cache_low(c, it.k.pmax);
+      float o[R / 8][4];
+#pragma unroll
+      for (int k = 0; k < R / 8; ++k) o[k][0] = o[k][1] = o[k][2] = o[k][3] = 0.f;
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      for (int i = it.t0; ok && i < it.t1; ++i, ++g) {
+        const int st = g % KS;
+        bool w = mbar_wait(&kv_full[st], (g / KS) & 1, abort_flag, c.status);
+        if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
+        const int32_t t0 = cache_tile(it.k, i) * KT + warp * 16;
+        if (t0 > it.k.pmax) {              // nothing of this warp's events is there
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&kv_empty[st]);
+          continue;
+        }
+        uint8_t* kv = sKV + st * C::KV_BYTES;
+        const uint32_t kv_addr = smem_u32(kv);
+        // S = Q C^T: two accumulators of 16 pairs x 8 events, even and odd steps apart
+        float s[2][2][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[0][j][e] = s[1][j][e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < R / 16; ++k) {
+          uint32_t b[4];
+          ldsm4(kv_addr + (k >> 2) * C::KV_SUB + k_row + (((2 * (k & 3) + k_chunk) ^ xr) << 4), b);
+          mma16816(s[k & 1][0], qa[k], b[0], b[1]);
+          mma16816(s[k & 1][1], qa[k], b[2], b[3]);
+        }
+        float v[2][4];                     // [event group j][row half * 2 + event]
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[j][e] = (s[0][j][e] + s[1][j][e]) * p.scale2;
+        bool poison[2] = {false, false};
+        if (it.k.pmin < t0 + 15 || low_max > t0) {
+          // some row hides some of the 16 events
+          bool odd = false;
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const bool fin = fabsf(v[j][e]) < INFINITY;
+              const int h = e >> 1;
+              const int32_t t = t0 + 8 * j + 2 * t4 + (e & 1);
+              const bool see = t <= pos[h] && (t >= low[h] || t < c.n_sink);
+              if (!fin && grp + 8 * h < rows) {
+                odd = true;
+                poison[h] |= see;
+              }
+              v[j][e] = see && fin ? v[j][e] : -INFINITY;
+            }
+          if (__any_sync(0xffffffffu, odd)) clear_rows<R>(kv, warp * 16);
+        }
+        // running maxima; O and the sums keep their base until one grows by more than
+        // 2^8 (a row that has seen nothing yet takes the first maximum it meets)
+        float mt[2];
+        bool grow = false;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          mt[h] = fmaxf(fmaxf(v[0][2 * h], v[0][2 * h + 1]), fmaxf(v[1][2 * h], v[1][2 * h + 1]));
+          mt[h] = fmaxf(mt[h], __shfl_xor_sync(0xffffffffu, mt[h], 1));
+          mt[h] = fmaxf(mt[h], __shfl_xor_sync(0xffffffffu, mt[h], 2));
+          grow |= mt[h] > m[h] + 8.f;
+        }
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float mn = fmaxf(m[h], mt[h]);
+            const float f = m[h] > -INFINITY ? ex2_approx(m[h] - mn) : 0.f;
+            m[h] = mn;
+            l[h] *= f;
+#pragma unroll
+            for (int k = 0; k < R / 8; ++k) {
+              o[k][2 * h] *= f;
+              o[k][2 * h + 1] *= f;
+            }
+          }
+        }
+        // weights, in bf16 for the product and unrounded in the sum
+        uint32_t pa[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float mu = m[h] > -INFINITY ? m[h] : 0.f;
+          const float a = ex2_approx(v[0][2 * h] - mu), b = ex2_approx(v[0][2 * h + 1] - mu);
+          const float d = ex2_approx(v[1][2 * h] - mu), e = ex2_approx(v[1][2 * h + 1] - mu);
+          l[h] += (a + b) + (d + e);
+          if (poison[h]) l[h] = NAN;
+          pa[h] = pack_bf16(a, b);
+          pa[2 + h] = pack_bf16(d, e);
+        }
+        // O += P C: 16 columns a step
+#pragma unroll
+        for (int k = 0; k < R / 16; ++k) {
+          uint32_t b[4];
+          ldsm4t(kv_addr + (k >> 2) * C::KV_SUB + v_row + (((2 * (k & 3) + v_chunk) ^ xr) << 4), b);
+          mma16816(o[2 * k], pa, b[0], b[1]);
+          mma16816(o[2 * k + 1], pa, b[2], b[3]);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&kv_empty[st]);
+      }
+      // ---- the warps' results meet (after an abort too: every warp makes the same
+      // number of meets, so none waits alone)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+        if (t4 == 0) {
+          sm_m[warp * MT + grp + 8 * h] = m[h];
+          sm_l[warp * MT + grp + 8 * h] = l[h];
+        }
+      }
+      meet_sync();
+      float f[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float mall = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < NW; ++k) mall = fmaxf(mall, sm_m[k * MT + grp + 8 * h]);
+        f[h] = m[h] > -INFINITY ? ex2_approx(m[h] - mall) : 0.f;
+      }
+      // sums 4 columns of a row; the rows past 8 only where there are any
+      const int halves = rows > 8 ? 2 : 1, row = threadIdx.x >> 4, c4 = threadIdx.x & 15;
+      float mall = -INFINITY, lall = 0.f;
+#pragma unroll
+      for (int k = 0; k < NW; ++k) mall = fmaxf(mall, sm_m[k * MT + row]);
+      const float mu = mall > -INFINITY ? mall : 0.f;
+#pragma unroll
+      for (int k = 0; k < NW; ++k)
+        lall = fmaf(sm_l[k * MT + row], ex2_approx(sm_m[k * MT + row] - mu), lall);
+      if (mall == INFINITY) lall = NAN;
+      const int64_t slot = ((int64_t)blockIdx.x * 2 + (it.starts ? 1 : 0)) * MT + row;
+      const float inv = lall != 0.f ? 1.f / lall : 0.f;
+#pragma unroll
+      for (int q = 0; q < R / 64; ++q) {
+        // column pairs XORed with the row, so that the 8 rows of a store fall on
+        // different banks
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (h >= halves) continue;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int r = grp + 8 * h;
+            ((float2*)meet)[(warp * MT + r) * 32 + ((4 * k + t4) ^ ((r & 7) << 2))] =
+                make_float2(o[8 * q + k][2 * h] * f[h], o[8 * q + k][2 * h + 1] * f[h]);
+          }
+        }
+        meet_sync();
+        if (row < rows) {
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int k = 0; k < NW; ++k) {
+            const float4 y = *(const float4*)(
+                meet + ((k * MT + row) * 32 + ((2 * c4) ^ ((row & 7) << 2))) * 2);
+            x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+          }
+          if (it.whole)
+            *(uint2*)((__nv_bfloat16*)p.out + (at0 + row) * R + q * 64 + c4 * 4) =
+                make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
+          else
+            *(float4*)(p.part_o + slot * R + q * 64 + c4 * 4) = x;
+        }
+        meet_sync();
+      }
+      if (c4 == 0 && row < rows) {
+        if (it.whole) {
+          const float l2 = lall != 0.f ? mall + log2f(lall) : -INFINITY;
+          if (p.lse) p.lse[at0 + row] = l2 * kLn2;
+          if (p.lse2) p.lse2[at0 + row] = l2;
+        } else {
+          p.part_ml[slot] = make_float2(mall, lall);
+        }
+      }
+      if (threadIdx.x == 0 && !it.whole && it.starts) {
+        join->pair0 = at0;
+        join->parts = it.parts;
+        join->rows = rows;
+      }
+    }
+  }
+}
+
+template <int R>
+cudaError_t launch_r(CacheAttn a, const CUtensorMap& tmC, int num_sms, cudaStream_t s) {
+  using C = Cfg<R>;
+  static uint64_t attr_devices = 0;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (!(attr_devices >> (dev & 63) & 1)) {
+    cudaError_t e = cudaFuncSetAttribute(cache_token_kernel<R>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+    if (e != cudaSuccess) return e;
+    // the register split waits for what the launch does not have
+    cudaFuncAttributes f;
+    e = cudaFuncGetAttributes(&f, cache_token_kernel<R>);
+    if (e != cudaSuccess) return e;
+    if (f.numRegs * 3 < 2 * kRegsConsume + kRegsProduce) return cudaErrorInvalidConfiguration;
+    attr_devices |= 1ull << (dev & 63);
+  }
+  cudaError_t e = launch_dependent(cache_token_kernel<R>, dim3(num_sms), dim3(kThreads), C::SMEM, s,
+                                   1, tmC, a);
+  if (e != cudaSuccess) return e;
+  return a.never_cut ? cudaSuccess : launch_cache_join(a, MT, num_sms, s);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_token(const CacheAttn& a, const CUtensorMap& tmC, int num_sms,
+                               cudaStream_t s) {
+  switch (a.c.r) {
+    case 64: return launch_r<64>(a, tmC, num_sms, s);
+    case 128: return launch_r<128>(a, tmC, num_sms, s);
+    case 256: return launch_r<256>(a, tmC, num_sms, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace llatte
