@@ -248,6 +248,12 @@ def _stream_ptr(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+# Address of a device's current stream; torch.cuda.current_stream builds an object
+# around it first.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 class Llatte:
     """A forward handle: weights (non-absorbed, pages' layout) are copied and
     absorbed at construction; `forward` runs the whole sequence module."""
@@ -592,7 +598,7 @@ class LatentCache:
                              "the pool's device")
         self.pool, self.mass, self.heads = pool, mass, int(heads)
         self.n_pages, self.page_size, self.rank = (int(n) for n in pool.shape)
-        self.device, self.dt = pool.device, pool.dtype
+        self.device, self.dt, self.index = pool.device, pool.dtype, pool.get_device()
         c = llatte_cache_dims()
         c.heads, c.rank, c.page_size, c.n_pages = self.heads, self.rank, self.page_size, self.n_pages
         c.dtype = LLATTE_BF16 if self.dt == torch.bfloat16 else LLATTE_FP32
@@ -612,28 +618,29 @@ class LatentCache:
     def uses_tensor_cores(self) -> bool:
         return self.lib.llatte_cache_uses_tensor_cores(self.h) == 1
 
-    def _tensor(self, name, t, dtype, shape):
-        if (not isinstance(t, torch.Tensor) or t.device != self.device or t.dtype != dtype
-                or not t.is_contiguous() or t.dim() != len(shape)
-                or any(n is not None and n != m for n, m in zip(shape, t.shape))):
-            want = ", ".join("*" if n is None else str(n) for n in shape)
-            raise ValueError(f"{name} must be a contiguous {dtype} [{want}] tensor on {self.device}")
-        return t
+    # A call is a few microseconds of device time at its smallest, so its checks are
+    # kept to one pass over each tensor; _refuse words the error.
+    def _fits(self, t, dtype, dims):
+        return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == self.index
+                and t.dim() == dims and t.is_contiguous())
+
+    def _refuse(self, name, dtype, shape):
+        raise ValueError(f"{name} must be a contiguous {dtype} [{shape}] tensor on {self.device}")
 
     def _view(self, table, lengths):
-        self._tensor("lengths", lengths, torch.int32, (None,))
-        B = int(lengths.shape[0])
-        self._tensor("table", table, torch.int32, (B, None))
-        return llatte_cache_view(table=table.data_ptr(), table_stride=int(table.shape[1]),
-                                 lengths=lengths.data_ptr(), B=B), B
+        if not self._fits(lengths, torch.int32, 1):
+            self._refuse("lengths", torch.int32, "*")
+        B = lengths.shape[0]
+        if not self._fits(table, torch.int32, 2) or table.shape[0] != B:
+            self._refuse("table", torch.int32, f"{B}, *")
+        return llatte_cache_view(table.data_ptr(), table.shape[1], lengths.data_ptr(), B), B
 
-    def _on(self, stream, *made):
-        """The stream a call runs on; tensors made here for it are kept until it is done."""
+    def _on(self, stream, made=None):
+        """The stream a call runs on; a tensor made here for it is kept until it is done."""
         if stream is None:
-            return _stream_ptr(torch.cuda.current_stream(self.device))
-        for t in made:
-            if t is not None and isinstance(stream, torch.cuda.Stream):
-                t.record_stream(stream)
+            return _raw_stream(self.index)
+        if made is not None and isinstance(stream, torch.cuda.Stream):
+            made.record_stream(stream)
         return _stream_ptr(stream)
 
     def append(self, x: torch.Tensor, offsets: torch.Tensor, table: torch.Tensor,
@@ -642,12 +649,15 @@ class LatentCache:
         """Rows x[offsets[u]:offsets[u + 1]] become user u's newest events (lengths
         counts them already); with `gain` each is RMS-normalised first."""
         v, B = self._view(table, lengths)
-        self._tensor("x", x, self.dt, (None, self.rank))
-        self._tensor("offsets", offsets, torch.int64, (B + 1,))
-        if gain is not None:
-            self._tensor("gain", gain, self.dt, (self.rank,))
-        rc = self.lib.llatte_cache_append(self.h, ctypes.byref(v), _ptr(x), int(x.shape[0]),
-                                          _ptr(offsets), _ptr(gain), float(eps), self._on(stream))
+        if not self._fits(x, self.dt, 2) or x.shape[1] != self.rank:
+            self._refuse("x", self.dt, f"*, {self.rank}")
+        if not self._fits(offsets, torch.int64, 1) or offsets.shape[0] != B + 1:
+            self._refuse("offsets", torch.int64, B + 1)
+        if gain is not None and (not self._fits(gain, self.dt, 1) or gain.shape[0] != self.rank):
+            self._refuse("gain", self.dt, self.rank)
+        rc = self.lib.llatte_cache_append(
+            self.h, ctypes.byref(v), x.data_ptr(), x.shape[0], offsets.data_ptr(),
+            None if gain is None else gain.data_ptr(), eps, self._on(stream))
         if rc != LLATTE_OK:
             raise LlatteError(rc, "llatte_cache_append")
 
@@ -663,20 +673,22 @@ class LatentCache:
         the first n_sink.  `lse` (float32 [rows, heads]) receives the log of the
         softmax denominators; `accumulate` adds all weights to `mass`."""
         v, B = self._view(table, lengths)
-        self._tensor("q", q, self.dt, (None, self.heads, self.rank))
-        rows = int(q.shape[0])
-        self._tensor("q_offsets", q_offsets, torch.int64, (B + 1,))
+        if not self._fits(q, self.dt, 3) or q.shape[1:] != (self.heads, self.rank):
+            self._refuse("q", self.dt, f"*, {self.heads}, {self.rank}")
+        rows = q.shape[0]
+        if not self._fits(q_offsets, torch.int64, 1) or q_offsets.shape[0] != B + 1:
+            self._refuse("q_offsets", torch.int64, B + 1)
         made = None
         if out is None:
             out = made = torch.empty_like(q)
-        self._tensor("out", out, self.dt, (rows, self.heads, self.rank))
-        if lse is not None:
-            self._tensor("lse", lse, torch.float32, (rows, self.heads))
-        a = llatte_cache_attn(q=q.data_ptr(), q_offsets=q_offsets.data_ptr(), rows=rows,
-                              n_cand=int(n_cand), scale=float(scale), window=int(window),
-                              n_sink=int(n_sink), out=out.data_ptr(),
-                              lse=lse.data_ptr() if lse is not None else None,
-                              accumulate=1 if accumulate else 0)
+        elif not self._fits(out, self.dt, 3) or out.shape != q.shape:
+            self._refuse("out", self.dt, f"{rows}, {self.heads}, {self.rank}")
+        if lse is not None and (not self._fits(lse, torch.float32, 2)
+                                or lse.shape != (rows, self.heads)):
+            self._refuse("lse", torch.float32, f"{rows}, {self.heads}")
+        a = llatte_cache_attn(q.data_ptr(), q_offsets.data_ptr(), rows, n_cand, scale, window,
+                              n_sink, out.data_ptr(), None if lse is None else lse.data_ptr(),
+                              1 if accumulate else 0)
         rc = self.lib.llatte_cache_attend(self.h, ctypes.byref(v), ctypes.byref(a),
                                           self._on(stream, made))
         if rc != LLATTE_OK:
@@ -695,17 +707,18 @@ class LatentCache:
         made = None
         if new_lengths is None:
             new_lengths = made = torch.empty_like(lengths)
-        self._tensor("new_lengths", new_lengths, torch.int32, (B,))
-        if dst_table is not None:
-            self._tensor("dst_table", dst_table, torch.int32, (B, None))
-        if kept is not None:
-            self._tensor("kept", kept, torch.int32, (B, int(budget)))
+        elif not self._fits(new_lengths, torch.int32, 1) or new_lengths.shape[0] != B:
+            self._refuse("new_lengths", torch.int32, B)
+        if dst_table is not None and (not self._fits(dst_table, torch.int32, 2)
+                                      or dst_table.shape[0] != B):
+            self._refuse("dst_table", torch.int32, f"{B}, *")
+        if kept is not None and (not self._fits(kept, torch.int32, 2)
+                                 or kept.shape != (B, budget)):
+            self._refuse("kept", torch.int32, f"{B}, {budget}")
         a = llatte_cache_evict_args(
-            budget=int(budget), n_sink=int(n_sink), n_recent=int(n_recent),
-            dst_table=dst_table.data_ptr() if dst_table is not None else None,
-            dst_stride=int(dst_table.shape[1]) if dst_table is not None else 0,
-            new_lengths=new_lengths.data_ptr(),
-            kept=kept.data_ptr() if kept is not None else None)
+            budget, n_sink, n_recent, None if dst_table is None else dst_table.data_ptr(),
+            0 if dst_table is None else dst_table.shape[1], new_lengths.data_ptr(),
+            None if kept is None else kept.data_ptr())
         rc = self.lib.llatte_cache_evict(self.h, ctypes.byref(v), ctypes.byref(a),
                                          self._on(stream, made))
         if rc != LLATTE_OK:
