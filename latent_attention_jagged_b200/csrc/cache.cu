@@ -26,8 +26,8 @@ struct llatte_cache {
   float* lse2;           // [max_rows, heads]
   bool tc;               // attention on the tensor cores
   CUtensorMap tmC;       // the pool, a page a box (tc)
-  float* part_o;         // [2 num_sms, kCacheBlockRows, rank] (tc)
-  float2* part_ml;       // [2 num_sms, kCacheBlockRows]
+  float* part_o;         // [2 num_sms, block rows, rank]
+  float2* part_ml;       // [2 num_sms, block rows]
   CacheJoin* join;       // [num_sms]
 };
 
@@ -308,12 +308,10 @@ CacheLayout cache_layout(const llatte_cache_dims& d) {
   L.count = take(sizeof(int32_t) * d.max_batch);
   L.list = take(sizeof(int32_t) * (size_t)d.max_batch * d.max_pages * d.page_size);
   L.lse2 = take(sizeof(float) * (size_t)d.max_rows * d.heads);
-  if (cache_uses_tc(d)) {
-    const size_t slots = (size_t)2 * kCacheCtas * kCacheBlockRows;
-    L.part_o = take(sizeof(float) * slots * d.rank);
-    L.part_ml = take(sizeof(float2) * slots);
-    L.join = take(sizeof(CacheJoin) * kCacheCtas);
-  }
+  const size_t slots = (size_t)2 * kCacheCtas * (cache_uses_tc(d) ? kCacheBlockRows : 64);
+  L.part_o = take(sizeof(float) * slots * d.rank);
+  L.part_ml = take(sizeof(float2) * slots);
+  L.join = take(sizeof(CacheJoin) * kCacheCtas);
   L.total = o;
   return L;
 }
@@ -400,10 +398,10 @@ int llatte_cache_create(llatte_cache** out, const llatte_cache_dims* dims, void*
   h->lse2 = (float*)(h->ws + L.lse2);
   h->num_sms = std::min(h->num_sms, kCacheCtas);
   h->tc = cache_uses_tc(*dims);
+  h->part_o = (float*)(h->ws + L.part_o);
+  h->part_ml = (float2*)(h->ws + L.part_ml);
+  h->join = (CacheJoin*)(h->ws + L.join);
   if (h->tc) {
-    h->part_o = (float*)(h->ws + L.part_o);
-    h->part_ml = (float2*)(h->ws + L.part_ml);
-    h->join = (CacheJoin*)(h->ws + L.join);
     const uint64_t rows = (uint64_t)dims->n_pages * dims->page_size;
     if (!make_tmap_bf16(&h->tmC, pool, rows, dims->rank, std::min(dims->page_size, kCacheBox))) {
       llatte_cache_destroy(h);
@@ -457,11 +455,11 @@ int llatte_cache_attend(llatte_cache* h, const llatte_cache_view* v, const llatt
   cudaStream_t s = (cudaStream_t)stream;
   a.part_o = h->part_o; a.part_ml = h->part_ml; a.join = h->join;
   const cudaError_t e = h->tc ? launch_cache_attn_tc(a, h->tmC, h->num_sms, s)
-                              : launch_cache_attn_simt(h->elem, a, s);
+                              : launch_cache_attn_simt(h->elem, a, h->num_sms, s);
   if (e != cudaSuccess) return LLATTE_ERR_CUDA;
   if (!p->accumulate) return LLATTE_OK;
   const cudaError_t m = h->tc ? launch_cache_mass_tc(a, h->tmC, h->num_sms, s)
-                              : launch_cache_mass_simt(h->elem, a, s);
+                              : launch_cache_mass_simt(h->elem, a, h->num_sms, s);
   if (m != cudaSuccess) return LLATTE_ERR_CUDA;
   return LLATTE_OK;
 }

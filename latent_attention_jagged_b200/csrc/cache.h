@@ -70,6 +70,15 @@ struct CacheEvict {
   int32_t* count;            // workspace: [B] kept events, -1 = nothing to move
 };
 
+// Most tiles of kt events that a block of mt pairs reads, as far as the host can tell.
+inline int64_t cache_most_tiles(const CacheCall& c, int mt, int kt) {
+  const int64_t t = (c.cap + kt - 1) / kt;
+  if (c.window == 0) return t;
+  const int64_t span = (int64_t)c.window + mt / c.heads;       // of the windows of its rows
+  const int64_t w = (span + kt - 1) / kt + 1 + ((int64_t)c.n_sink + kt - 1) / kt;
+  return t < w ? t : w;
+}
+
 cudaError_t launch_cache_append(int elem, const CacheAppend& a, cudaStream_t s);
 cudaError_t launch_cache_evict(int elem, const CacheEvict& a, cudaStream_t s);
 // Tensor-core attention (bf16, rank 64, 128 or 256); tmC: the pool as a tensor
@@ -87,7 +96,7 @@ cudaError_t launch_cache_join(const CacheAttn& a, int mt, int num_sms, cudaStrea
 constexpr int kCacheBox = 64;              // rows of a box of tmC, or a page if that is smaller
 constexpr int kCacheBlockRows = 128;       // largest block of pairs
 // CUDA-core attention (any rank up to 256, both types) and its accumulation.
-cudaError_t launch_cache_attn_simt(int elem, const CacheAttn& a, cudaStream_t s);
-cudaError_t launch_cache_mass_simt(int elem, const CacheAttn& a, cudaStream_t s);
+cudaError_t launch_cache_attn_simt(int elem, const CacheAttn& a, int num_sms, cudaStream_t s);
+cudaError_t launch_cache_mass_simt(int elem, const CacheAttn& a, int num_sms, cudaStream_t s);
 
 }  // namespace llatte

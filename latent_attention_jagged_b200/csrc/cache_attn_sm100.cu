@@ -735,21 +735,12 @@ cudaError_t launch_rm(const CacheAttn& a, const CUtensorMap& tmC, int num_sms, c
   return a.never_cut ? cudaSuccess : launch_cache_join(a, MT, num_sms, s);
 }
 
-// Most tiles that a block of mt pairs reads, as far as the host can tell.
-int64_t most_tiles(const CacheCall& c, int mt) {
-  int64_t t = (c.cap + KT - 1) / KT;
-  if (c.window > 0)
-    t = std::min<int64_t>(t, ((int64_t)c.window + mt / c.heads + KT) / KT + 1 +
-                                 ((int64_t)c.n_sink + KT - 1) / KT);
-  return t;
-}
-
 template <int R>
 cudaError_t launch_r(CacheAttn a, const CUtensorMap& tmC, int num_sms, cudaStream_t s) {
   // Blocks of up to 4 tiles are not cut: the tiles that a CTA may have too many of
   // take less time than the launch that would join the parts.
   a.min_quota = 1;
-  a.never_cut = most_tiles(a.c, 128) <= 4;
+  a.never_cut = cache_most_tiles(a.c, 128, KT) <= 4;
   // few pairs a user on average: see cache_token_sm100.cu
   if (a.c.rows * a.c.heads <= 16 * (int64_t)a.c.B) return launch_cache_token(a, tmC, num_sms, s);
 
