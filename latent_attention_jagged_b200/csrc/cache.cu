@@ -7,6 +7,7 @@
 
 #include "cache.h"
 #include "cache_call.cuh"
+#include "tc_common.cuh"
 #include "tc_gemm.h"
 
 using namespace llatte;
@@ -35,52 +36,98 @@ namespace llatte {
 namespace {
 
 // ---------------------------------------------------------------- append
-// c = x / sqrt(mean(x^2) + eps) * g.  One warp per row, its 16-byte vectors
-// spread over the lanes and kept in registers between the sum and the store.
-template <typename T, int NV>
+// c = x / sqrt(mean(x^2) + eps) * g.  Bound by reading and writing the rows; what a row
+// waits for is its place (offsets -> user -> length, page).  So a warp takes 4 steps
+// of 32 / G rows (G lanes a row, NV 16-byte vectors a lane), asks for all of them
+// before it looks for their users, and one lane per row finds the place: a 32-way
+// search by the warp for its first and last row, the rest between the two.
+template <typename T, int G, int NV>
 __global__ void __launch_bounds__(256) cache_append_kernel(CacheAppend a) {
-  constexpr int EV = 16 / sizeof(T);
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  constexpr int EV = 16 / sizeof(T), STEP = 32 / G, ROWS = 4 * STEP;
   const CacheCall& c = a.c;
-  if (row < c.qoff[0] || row >= min(c.rows, c.qoff[c.B])) return;
-  const int u = segment_of(c.qoff, c.B, row);
-  const CacheUser x = cache_user(c, u);
-  if (row < x.row0 || row - x.row0 >= x.n) return;
-  const int32_t slot = x.len - x.n + (int32_t)(row - x.row0);
-  const int64_t dst = cache_row(c, c.table, c.stride, u, slot);
-  if (dst < 0) return;
-  const int nvec = c.r / EV;
-  uint4 v[NV];
-  float ss = 0.f;
+  const int lane = threadIdx.x & 31;
+  const int64_t row0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * ROWS;
+  // the search below may pass by a faulty user: the last block looks at them all
+  if (blockIdx.x == gridDim.x - 1)
+    for (int u = threadIdx.x; u < c.B; u += 256) cache_user(c, u);
+  if (row0 >= c.rows) return;
+  const int nvec = c.r / EV, sub = lane / G, k0 = lane % G;
+  uint4 v[4][NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int k = lane + 32 * i;
-    v[i] = make_uint4(0, 0, 0, 0);
-    if (k < nvec) v[i] = __ldg((const uint4*)a.x + row * nvec + k);
-    const T* e = (const T*)&v[i];
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < EV; ++j) ss = fmaf(to_f(e[j]), to_f(e[j]), ss);
+    for (int j = 0; j < NV; ++j) {
+      const int64_t row = row0 + i * STEP + sub;
+      const int k = k0 + G * j;
+      v[i][j] = make_uint4(0, 0, 0, 0);
+      if (row < c.rows && k < nvec) v[i][j] = __ldg((const uint4*)a.x + row * nvec + k);
+    }
+  // the last user whose rows start at or before `row` (0 when there is none)
+  auto find = [&](int64_t row) {
+    int lo = 0, n = c.B;
+    while (n > 1) {
+      const int step = (n + 31) / 32;
+      const bool le = lane * step < n && __ldg(c.qoff + lo + lane * step) <= row;
+      const uint32_t m = __ballot_sync(0xffffffffu, le);
+      const int k = m ? 31 - __clz(m) : 0;
+      n = min(step, n - k * step);
+      lo += k * step;
+    }
+    return lo;
+  };
+  const int64_t last = min(row0 + ROWS, c.rows) - 1;
+  const int u0 = find(row0), u1 = __ldg(c.qoff + min(u0 + 1, c.B)) > last ? u0 : find(last);
+  int64_t dst = -1;
+  if (lane < ROWS && row0 + lane <= last) {
+    const int64_t row = row0 + lane;
+    int lo = u0, hi = max(u0, u1);
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (__ldg(c.qoff + mid) <= row) lo = mid; else hi = mid - 1;
+    }
+    const CacheUser x = cache_user(c, lo);
+    if (row >= x.row0 && row - x.row0 < x.n)
+      dst = cache_row(c, c.table, c.stride, lo, x.len - x.n + (int32_t)(row - x.row0));
+    if (dst >= 0 && a.mass) a.mass[dst] = 0.f;
   }
+  float g[NV][EV];
   if (a.gain) {
-    const float inv = 1.f / sqrtf(warp_sum(ss) / (float)c.r + a.eps);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int k = lane + 32 * i;
-      if (k >= nvec) continue;
-      const uint4 gv = __ldg((const uint4*)a.gain + k);
-      const T* g = (const T*)&gv;
-      T* e = (T*)&v[i];
+    for (int j = 0; j < NV; ++j) {
+      const int k = k0 + G * j;
+      const uint4 gv = k < nvec ? __ldg((const uint4*)a.gain + k) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int j = 0; j < EV; ++j) e[j] = from_f<T>(to_f(e[j]) * inv * to_f(g[j]));
+      for (int e = 0; e < EV; ++e) g[j][e] = to_f(((const T*)&gv)[e]);
     }
   }
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int k = lane + 32 * i;
-    if (k < nvec) ((uint4*)a.pool)[dst * nvec + k] = v[i];
+  for (int i = 0; i < 4; ++i) {
+    const int64_t to = __shfl_sync(0xffffffffu, dst, i * STEP + sub);
+    if (a.gain) {
+      float ss = 0.f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < EV; ++e) {
+          const float f = to_f(((const T*)&v[i][j])[e]);
+          ss = fmaf(f, f, ss);
+        }
+#pragma unroll
+      for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const float inv = 1.f / sqrtf(ss / (float)c.r + a.eps);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        T* e = (T*)&v[i][j];
+#pragma unroll
+        for (int b = 0; b < EV; ++b) e[b] = from_f<T>(to_f(e[b]) * inv * g[j][b]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int k = k0 + G * j;
+      if (to >= 0 && k < nvec) ((uint4*)a.pool)[to * nvec + k] = v[i][j];
+    }
   }
-  if (a.mass && lane == 0) a.mass[dst] = 0.f;
 }
 
 // ---------------------------------------------------------------- evict
@@ -93,39 +140,152 @@ __device__ __forceinline__ uint32_t mass_key(float f) {
 
 constexpr int kSelThreads = 512;
 
-// Kept slots of one user per block.  The threshold, the need-th largest key of
-// the events that do not stay anyway, is found digit by digit (8 bits, from the
-// top) with a histogram of the keys that share the digits found so far; then
-// one pass in slot order writes the kept slots, events at the threshold going
-// to the earliest slots.
+// Kept slots of one user per block; left out, short and absent users.  Returns false
+// when the block is done.
+__device__ __forceinline__ bool select_start(const CacheEvict& a, int u, CacheUser* x) {
+  const int tid = threadIdx.x;
+  *x = cache_user(a.c, u);
+  const bool left_out = a.c.lengths[u] != x->len;
+  const int T = x->len, K = a.budget;
+  __syncthreads();                      // new_lengths may be the lengths just read
+  if (tid == 0) a.count[u] = left_out ? 0 : min(T, K);
+  if (left_out) return false;
+  if (tid == 0) a.new_lengths[u] = min(T, K);
+  if (T > K) return true;
+  for (int t = tid; t < T; t += kSelThreads) {
+    a.list[(int64_t)u * a.list_stride + t] = t;
+    if (a.kept) a.kept[(int64_t)u * K + t] = t;
+  }
+  return false;
+}
+
+// Exclusive sum of v over the block's threads, and the total in *all.
+__device__ __forceinline__ int block_scan(int v, int* warps, int* all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) warps[warp] = incl;
+  __syncthreads();
+  const int w = lane < kSelThreads / 32 ? warps[lane] : 0;
+  *all = __reduce_add_sync(0xffffffffu, w);
+  const int before = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
+  __syncthreads();                      // warps[] may be written again
+  return before + incl - v;
+}
+
+// Users of up to NK * kSelThreads events: the keys are read once and stay in
+// registers, NK neighbours a thread.  The threshold, the need-th largest key of the
+// events that do not stay anyway, is found bit by bit from the highest bit in which
+// the keys differ: the largest value that `need` keys reach.  Then two sums over the
+// block place the kept slots in order, events at the threshold going to the earliest
+// slots.  (Digits with histograms in shared memory took 31 us for 256 users of 700 to
+// 1600 events: heavy-tailed masses fall into a few bins.)
+template <int NK>
 __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(CacheEvict a) {
+  __shared__ int s_warp[2][kSelThreads / 32];
+  const CacheCall& c = a.c;
+  const int u = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  CacheUser x;
+  if (!select_start(a, u, &x)) return;
+  const int T = x.len, K = a.budget, lo = c.n_sink, hi = T - a.n_recent;   // [lo, hi): may go
+  const int need = K - c.n_sink - a.n_recent;
+  const int t0 = threadIdx.x * NK;
+  uint32_t key[NK];
+  uint32_t top = 0, low = 0xffffffffu;
+#pragma unroll
+  for (int i = 0; i < NK; ++i) {
+    const int t = t0 + i;
+    key[i] = 0;
+    if (t >= lo && t < hi && need > 0) {
+      const int64_t row = cache_row(c, c.table, c.stride, u, t);
+      key[i] = row < 0 ? 0u : mass_key(a.mass[row]);
+      top = max(top, key[i]);
+      low = min(low, key[i]);
+    }
+  }
+  uint32_t thr = 0;
+  int n_eq = 0;                         // events at the threshold that stay
+  if (need > 0) {
+    top = __reduce_max_sync(0xffffffffu, top);
+    low = __reduce_min_sync(0xffffffffu, low);
+    if (lane == 0) {
+      s_warp[0][warp] = (int)top;
+      s_warp[1][warp] = (int)low;
+    }
+    __syncthreads();
+    top = __reduce_max_sync(0xffffffffu, (uint32_t)s_warp[0][lane & (kSelThreads / 32 - 1)]);
+    low = __reduce_min_sync(0xffffffffu, (uint32_t)s_warp[1][lane & (kSelThreads / 32 - 1)]);
+    __syncthreads();
+    // events of the range that reach v
+    int turn = 0;
+    auto reach = [&](uint32_t v) -> int {
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < NK; ++i) n += t0 + i >= lo && t0 + i < hi && key[i] >= v;
+      n = __reduce_add_sync(0xffffffffu, n);
+      int* w = s_warp[turn];
+      turn ^= 1;                        // the last round's sums may still be read
+      if (lane == 0) w[warp] = n;
+      __syncthreads();
+      return __reduce_add_sync(0xffffffffu, lane < kSelThreads / 32 ? w[lane] : 0);
+    };
+    const int bits = 32 - __clz(top ^ low);          // the keys share what is above
+    thr = bits == 32 ? 0u : low >> bits << bits;
+    for (int b = bits - 1; b >= 0; --b) {
+      const uint32_t v = thr | 1u << b;
+      if (reach(v) >= need) thr = v;
+    }
+    n_eq = need - (thr == 0xffffffffu ? 0 : reach(thr + 1));
+    __syncthreads();
+  }
+  int eq = 0;
+#pragma unroll
+  for (int i = 0; i < NK; ++i) eq += need > 0 && t0 + i >= lo && t0 + i < hi && key[i] == thr;
+  int all;
+  int before = block_scan(eq, s_warp[0], &all);
+  uint32_t keep = 0;
+#pragma unroll
+  for (int i = 0; i < NK; ++i) {
+    const int t = t0 + i;
+    if (t >= T) continue;
+    if (t < lo || t >= hi) {
+      keep |= 1u << i;
+    } else if (need > 0) {
+      if (key[i] > thr || (key[i] == thr && before < n_eq)) keep |= 1u << i;
+      before += key[i] == thr;
+    }
+  }
+  int at = block_scan(__popc(keep), s_warp[1], &all);
+  int32_t* list = a.list + (int64_t)u * a.list_stride;
+  int32_t* kept = a.kept ? a.kept + (int64_t)u * K : nullptr;
+#pragma unroll
+  for (int i = 0; i < NK; ++i)
+    if ((keep >> i) & 1) {
+      list[at] = t0 + i;
+      if (kept) kept[at] = t0 + i;
+      ++at;
+    }
+}
+
+// Longer users: the threshold is found digit by digit (8 bits, from the top) with a
+// histogram of the keys that share the digits found so far, reading the masses again
+// for every digit; then one pass in slot order writes the kept slots.
+__global__ void __launch_bounds__(kSelThreads) cache_select_long_kernel(CacheEvict a) {
   __shared__ int hist[256];
   __shared__ uint32_t s_prefix;
   __shared__ int s_need;
   __shared__ int s_warp[2][kSelThreads / 32];
   const CacheCall& c = a.c;
   const int u = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const CacheUser x = cache_user(c, u);
-  const bool left_out = c.lengths[u] != x.len;
+  CacheUser x;
+  if (!select_start(a, u, &x)) return;
   const int T = x.len, K = a.budget;
-  __syncthreads();                      // new_lengths may be the lengths just read
-  if (left_out) {
-    if (tid == 0) a.count[u] = 0;
-    return;
-  }
   int32_t* list = a.list + (int64_t)u * a.list_stride;
   int32_t* kept = a.kept ? a.kept + (int64_t)u * K : nullptr;
-  if (tid == 0) {
-    a.count[u] = min(T, K);
-    a.new_lengths[u] = min(T, K);
-  }
-  if (T <= K) {
-    for (int t = tid; t < T; t += kSelThreads) {
-      list[t] = t;
-      if (kept) kept[t] = t;
-    }
-    return;
-  }
   const int lo = c.n_sink, hi = T - a.n_recent;       // [lo, hi): may go
   auto key_of = [&](int t) -> uint32_t {
     const int64_t row = cache_row(c, c.table, c.stride, u, t);
@@ -192,7 +352,7 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(CacheEvict a)
   }
 }
 
-// Moves the kept rows.  A block owns one 64-byte column slice of one user's
+// Moves the kept rows in place.  A block owns one 64-byte column slice of one user's
 // rows (the last slice index: the masses) and walks them in order, so that
 // packing in place is safe without any other block: row i comes from a slot
 // >= i, and a step's rows are all read before any of them is written.
@@ -201,11 +361,11 @@ constexpr int kSliceBytes = 64;
 
 __global__ void __launch_bounds__(kMoveThreads)
 cache_move_kernel(CacheEvict a, int row_bytes, int slices) {
+  tc::pdl_wait();
   const CacheCall& c = a.c;
   const int u = blockIdx.y, slice = blockIdx.x;
   const int n = a.count[u];
   const int32_t* list = a.list + (int64_t)u * a.list_stride;
-  const bool in_place = a.dst_table == c.table;
   if (slice == slices) {
     for (int i0 = 0; i0 < n; i0 += kMoveThreads) {
       const int i = i0 + threadIdx.x;
@@ -214,7 +374,7 @@ cache_move_kernel(CacheEvict a, int row_bytes, int slices) {
       if (i < n) {
         const int t = list[i];
         const int64_t src = cache_row(c, c.table, c.stride, u, t);
-        dst = in_place && t == i ? -1 : cache_row(c, a.dst_table, a.dst_stride, u, i);
+        dst = t == i ? -1 : cache_row(c, a.dst_table, a.dst_stride, u, i);
         v = src < 0 ? 0.f : a.mass[src];
       }
       __syncthreads();
@@ -232,7 +392,7 @@ cache_move_kernel(CacheEvict a, int row_bytes, int slices) {
     if (i < n && byte < row_bytes) {
       const int t = list[i];
       const int64_t src = cache_row(c, c.table, c.stride, u, t);
-      dst = in_place && t == i ? -1 : cache_row(c, a.dst_table, a.dst_stride, u, i);
+      dst = t == i ? -1 : cache_row(c, a.dst_table, a.dst_stride, u, i);
       if (src >= 0) v = *(const uint4*)((const char*)a.pool + src * row_bytes + byte);
     }
     __syncthreads();
@@ -240,13 +400,59 @@ cache_move_kernel(CacheEvict a, int row_bytes, int slices) {
   }
 }
 
+// Moves the kept rows to other pages: a warp copies whole rows, 4 at a time.
+__global__ void __launch_bounds__(kMoveThreads)
+cache_copy_kernel(CacheEvict a, int nvec) {
+  tc::pdl_wait();
+  const CacheCall& c = a.c;
+  const int u = blockIdx.y, lane = threadIdx.x & 31;
+  const int n = a.count[u];
+  const int32_t* list = a.list + (int64_t)u * a.list_stride;
+  for (int i0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * 32; i0 < n; i0 += gridDim.x * 256) {
+    // lane l: place of row i0 + l
+    int64_t src = -1, dst = -1;
+    if (i0 + lane < n) {
+      src = cache_row(c, c.table, c.stride, u, list[i0 + lane]);
+      dst = cache_row(c, a.dst_table, a.dst_stride, u, i0 + lane);
+      if (dst >= 0) a.mass[dst] = src < 0 ? 0.f : a.mass[src];
+    }
+    const int rows = min(32, n - i0);
+    for (int r = 0; r < rows; r += 4) {
+      int64_t s[4], d[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        s[k] = __shfl_sync(0xffffffffu, src, r + k);
+        d[k] = __shfl_sync(0xffffffffu, dst, r + k);
+      }
+      for (int col = lane; col < nvec; col += 32) {
+        uint4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          v[k] = make_uint4(0, 0, 0, 0);
+          if (s[k] >= 0) v[k] = __ldcs((const uint4*)a.pool + s[k] * nvec + col);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (d[k] >= 0) ((uint4*)a.pool)[d[k] * nvec + col] = v[k];
+      }
+    }
+  }
+}
+
+template <typename T, int G, int NV>
+cudaError_t append_g(const CacheAppend& a, cudaStream_t s) {
+  constexpr int rows = 8 * 4 * 32 / G;
+  cache_append_kernel<T, G, NV><<<(unsigned)((a.c.rows + rows - 1) / rows), 256, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
 template <typename T>
 cudaError_t append_t(const CacheAppend& a, cudaStream_t s) {
-  const unsigned blocks = (unsigned)((a.c.rows + 7) / 8);
   const int nvec = a.c.r * (int)sizeof(T) / 16;
-  if (nvec <= 32) cache_append_kernel<T, 1><<<blocks, 256, 0, s>>>(a);
-  else cache_append_kernel<T, 2><<<blocks, 256, 0, s>>>(a);
-  return cudaGetLastError();
+  if (nvec <= 8) return append_g<T, 8, 1>(a, s);
+  if (nvec <= 16) return append_g<T, 16, 1>(a, s);
+  if (nvec <= 32) return append_g<T, 32, 1>(a, s);
+  return append_g<T, 32, 2>(a, s);
 }
 
 }  // namespace
@@ -256,11 +462,19 @@ cudaError_t launch_cache_append(int elem, const CacheAppend& a, cudaStream_t s) 
 }
 
 cudaError_t launch_cache_evict(int elem, const CacheEvict& a, cudaStream_t s) {
-  cache_select_kernel<<<a.c.B, kSelThreads, 0, s>>>(a);
+  const int64_t most = std::min<int64_t>(a.c.cap, a.budget);    // kept events of a user
+  if (a.c.cap <= 4 * kSelThreads) cache_select_kernel<4><<<a.c.B, kSelThreads, 0, s>>>(a);
+  else if (a.c.cap <= 16 * kSelThreads) cache_select_kernel<16><<<a.c.B, kSelThreads, 0, s>>>(a);
+  else cache_select_long_kernel<<<a.c.B, kSelThreads, 0, s>>>(a);
   const int row_bytes = a.c.r * elem;
+  if (a.dst_table != a.c.table) {
+    const int blocks = (int)std::min<int64_t>((most + 255) / 256, 64);
+    return tc::launch_dependent(cache_copy_kernel, dim3(blocks, a.c.B), dim3(kMoveThreads), 0, s, 1,
+                                a, row_bytes / 16);
+  }
   const int slices = (row_bytes + kSliceBytes - 1) / kSliceBytes;
-  cache_move_kernel<<<dim3(slices + 1, a.c.B), kMoveThreads, 0, s>>>(a, row_bytes, slices);
-  return cudaGetLastError();
+  return tc::launch_dependent(cache_move_kernel, dim3(slices + 1, a.c.B), dim3(kMoveThreads), 0, s,
+                              1, a, row_bytes, slices);
 }
 
 }  // namespace llatte
