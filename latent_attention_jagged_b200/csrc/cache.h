@@ -92,6 +92,8 @@ cudaError_t launch_cache_mass_tc(const CacheAttn& a, const CUtensorMap& tmC, int
 // of a block).
 cudaError_t launch_cache_token(const CacheAttn& a, const CUtensorMap& tmC, int num_sms,
                                cudaStream_t s);
+cudaError_t launch_cache_mass_token(const CacheAttn& a, const CUtensorMap& tmC, int num_sms,
+                                    cudaStream_t s);
 cudaError_t launch_cache_join(const CacheAttn& a, int mt, int num_sms, cudaStream_t s);
 constexpr int kCacheBox = 64;              // rows of a box of tmC, or a page if that is smaller
 constexpr int kCacheBlockRows = 128;       // largest block of pairs

@@ -28,6 +28,7 @@
 
 #include "cache.h"
 #include "cache_call.cuh"
+#include "cache_issue.cuh"
 #include "cache_sched.cuh"
 #include "tc_common.cuh"
 #include "tc_drain.cuh"
@@ -127,19 +128,6 @@ __device__ __forceinline__ void clear_rows(uint8_t* kv, uint32_t sub) {
       for (int j = 0; j < 8; ++j) ((uint4*)(kv + s * sub + k * 128))[j] = make_uint4(0, 0, 0, 0);
   }
   fence_proxy_async_smem();
-}
-
-// One lane of a converged warp, and a wait that the warp agrees on.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok));
-  return ok != 0;
-}
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity,
-                                          volatile int* abort_flag, int32_t* status) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
 }
 
 // 32 bytes to dst: one store where it is aligned to them (whole sectors, so rows

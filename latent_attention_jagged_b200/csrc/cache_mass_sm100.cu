@@ -18,6 +18,7 @@
 
 #include "cache.h"
 #include "cache_call.cuh"
+#include "cache_issue.cuh"
 #include "cache_sched.cuh"
 #include "tc_common.cuh"
 #include "tc_drain.cuh"
@@ -191,42 +192,43 @@ cache_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t IDESC = idesc_bf16(128, NP, false, false);
-      uint32_t kn = 0, qn = 0;
-      bool ok = true;
-      CacheItems<Line> items;
-      items.start(c, run);
-      CacheItem<Line> it;
-      while (ok && items.next(c, it)) {
-        const int ks = kn % KS;
-        if (!mbar_wait(&k_full[ks], (kn / KS) & 1, abort_flag, c.status)) break;
-        const uint32_t k_addr = smem_u32(sK + ks * C::K_BYTES);
-        for (int i = it.t0; i < it.t1; ++i, ++qn) {
-          const int qs = qn % QS, sb = qn % SB;
-          if (!mbar_wait(&q_full[qs], (qn / QS) & 1, abort_flag, c.status) ||
-              !mbar_wait(&s_empty[sb], ((qn / SB) & 1) ^ 1, abort_flag, c.status)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t q_addr = smem_u32(sQ + qs * C::Q_BYTES);
+    // the warp stays converged and one lane issues (see cache_attn_sm100.cu)
+    constexpr uint32_t IDESC = idesc_bf16(128, NP, false, false);
+    const bool elect = elect_one();
+    uint32_t kn = 0, qn = 0;
+    bool ok = true;
+    CacheItems<Line> items;
+    items.start(c, run);
+    CacheItem<Line> it;
+    while (ok && items.next(c, it)) {
+      const int ks = kn % KS;
+      if (!warp_wait(&k_full[ks], (kn / KS) & 1, abort_flag, c.status)) break;
+      const uint64_t ad = sdesc_sw128(smem_u32(sK + ks * C::K_BYTES), 16, 1024);
+      for (int i = it.t0; i < it.t1; ++i, ++qn) {
+        const int qs = qn % QS, sb = qn % SB;
+        ok = warp_wait(&q_full[qs], (qn / QS) & 1, abort_flag, c.status) &&
+             warp_wait(&s_empty[sb], ((qn / SB) & 1) ^ 1, abort_flag, c.status);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t bd = sdesc_sw128(smem_u32(sQ + qs * C::Q_BYTES), 16, 1024);
+        const bool last = i == it.t1 - 1;
+        if (elect) {
 #pragma unroll
-          for (int k = 0; k < R / 16; ++k) {
-            const uint64_t ad = sdesc_sw128(k_addr + (k >> 2) * C::KSUB + (k & 3) * 32, 16, 1024);
-            const uint64_t bd = sdesc_sw128(q_addr + (k >> 2) * C::QSUB + (k & 3) * 32, 16, 1024);
-            umma_bf16(tmem + sb * NP, ad, bd, IDESC, k > 0 ? 1u : 0u);
-          }
+          for (int k = 0; k < R / 16; ++k)
+            umma_bf16(tmem + sb * NP, ad + (((k >> 2) * C::KSUB + (k & 3) * 32) >> 4),
+                      bd + (((k >> 2) * C::QSUB + (k & 3) * 32) >> 4), IDESC, k > 0 ? 1u : 0u);
           umma_commit(&s_full[sb]);
           umma_commit(&q_empty[qs]);
+          if (last) umma_commit(&k_empty[ks]);
         }
-        if (ok) umma_commit(&k_empty[ks]);
-        ++kn;
+        __syncwarp();
       }
-      umma_commit(drain);
-      int dummy = 0;
-      mbar_wait(drain, 0, &dummy, c.status);
+      ++kn;
     }
+    if (elect) umma_commit(drain);
+    __syncwarp();
+    int dummy = 0;
+    mbar_wait(drain, 0, &dummy, c.status);
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax
@@ -367,7 +369,8 @@ cudaError_t launch_rn(const CacheAttn& a, const CUtensorMap& tmC, int num_sms, c
 
 template <int R>
 cudaError_t launch_r(const CacheAttn& a, const CUtensorMap& tmC, int num_sms, cudaStream_t s) {
-  if (a.c.rows * a.c.heads <= 32 * (int64_t)a.c.B) return launch_rn<R, 32>(a, tmC, num_sms, s);
+  if (a.c.rows * a.c.heads <= 16 * (int64_t)a.c.B)
+    return launch_cache_mass_token(a, tmC, num_sms, s);
   return launch_rn<R, 128>(a, tmC, num_sms, s);
 }
 

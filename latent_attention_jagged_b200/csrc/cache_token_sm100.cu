@@ -413,6 +413,175 @@ cache_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn p) {
   }
 }
 
+// Accumulated weights of few new rows: as in cache_mass_sm100.cu the scores are computed
+// again transposed, here with mma.sync: a warp's 16 events are the m16 operand, the
+// pairs come in groups of 8 columns, and the weights of an event are the sum over the
+// columns of its row.  Nothing but the tiles' arrival is waited for.  A user's pairs
+// beyond 16 take another pass over the tile in shared memory.
+template <int R>
+__global__ void __launch_bounds__(kThreads, 1)
+cache_mass_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn p) {
+  using C = Cfg<R>;
+  using Line = ByTiles<MT, KT>;
+  constexpr int RSUB = C::RSUB, KS = C::KS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* sKV = smem;
+  uint64_t* bars = (uint64_t*)(sKV + KS * C::KV_BYTES + C::MEET);
+  uint64_t* kv_full = bars;                // [KS]
+  uint64_t* kv_empty = kv_full + KS;       // [KS]
+  volatile int* abort_flag = (volatile int*)(kv_empty + KS);
+  CacheSplit* split = (CacheSplit*)(kv_empty + KS + 1);
+
+  pdl_trigger();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const CacheCall& c = p.c;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < KS; ++s) { mbar_init(&kv_full[s], 1); mbar_init(&kv_empty[s], NW); }
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmC);
+  }
+  pdl_wait();
+  // no tile is cut: two CTAs that add to one event would do so in any order
+  cache_split<Line>(c, 1, true, *(CacheSplitSpace*)sKV, split);
+  fence_proxy_async_smem();
+  __syncthreads();
+  const CacheSplit run = *split;
+  CacheItems<Line> items;
+  items.start(c, run);
+  CacheItem<Line> it;
+  if (warp == NW) {
+    uint32_t g = 0;
+    const int32_t P = min(1 << c.page_shift, kCacheBox);
+    const int np = KT / P;
+    const int32_t outside = c.n_pages << c.page_shift;
+    bool ok = true;
+    while (ok && items.next(c, it)) {
+      int32_t y = outside;
+      const int32_t t = it.k.tile * KT + lane * P;
+      if (lane < np && cache_seen(c, it.k.all, t, t + P)) {
+        const int32_t page = __ldg(c.table + (int64_t)it.u * c.stride + (t >> c.page_shift));
+        if ((uint32_t)page < (uint32_t)c.n_pages)
+          y = (page << c.page_shift) + (t & ((1 << c.page_shift) - 1));
+        else
+          atomicOr(c.status, LLATTE_DEV_BAD_ID);
+      }
+      const int st = g % KS;
+      if (lane == 0) {
+        ok = mbar_wait(&kv_empty[st], ((g / KS) & 1) ^ 1, abort_flag, c.status);
+        if (ok) mbar_arrive_expect_tx(&kv_full[st], C::KV_BYTES);
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      if (lane < np) {
+        uint8_t* dst = sKV + st * C::KV_BYTES + lane * P * 128;
+#pragma unroll
+        for (int s = 0; s < RSUB; ++s)
+          tma_load_2d(&tmC, &kv_full[st], dst + s * C::KV_SUB, s * 64, y);
+      }
+      ++g;
+    }
+    __syncwarp();
+    if (lane == 0 && *abort_flag) drain_ring(kv_full, KS, g, c.status);
+    __syncwarp();
+  } else if (warp < NW) {
+    const int grp = lane >> 2, t4 = lane & 3;          // event (and event + 8), pair column
+    // ldmatrix rows of this lane: events 8 * (lane / 8 % 2) + lane % 8, chunk lane / 16
+    const uint32_t k_row = (warp * 16 + (((lane >> 3) & 1) << 3) + (lane & 7)) * 128;
+    const uint32_t k_chunk = lane >> 4, xr = lane & 7;
+    uint32_t g = 0;
+    int held_u = -1, held_b = -1;                      // whose queries qb holds
+    uint32_t qb[R / 16][4];
+    float lse[2][2];
+    int32_t pos[2][2];
+    while (items.next(c, it)) {
+      const int st = g % KS;
+      bool w = mbar_wait(&kv_full[st], (g / KS) & 1, abort_flag, c.status);
+      if (!__all_sync(0xffffffffu, w)) break;
+      const int32_t t0 = it.k.tile * KT + warp * 16;
+      const uint32_t kv_addr = smem_u32(sKV + st * C::KV_BYTES);
+      const int32_t pairs = it.x.n * c.heads;
+      float sum[2] = {0.f, 0.f};                       // of events grp and grp + 8
+      for (int b = it.k.first; b <= it.k.last && t0 <= it.k.all.pmax; ++b) {
+        if (it.u != held_u || b != held_b) {
+          // 16 pairs as two B operands of 8 columns; pairs past the last are zeros
+          held_u = it.u;
+          held_b = b;
+          const int64_t at0 = it.x.row0 * c.heads + (int64_t)b * MT;
+          const int rows = min(MT, pairs - b * MT);
+#pragma unroll
+          for (int k = 0; k < R / 16; ++k) {
+            const uint32_t* q0 =
+                (const uint32_t*)((const __nv_bfloat16*)p.q + (at0 + grp) * R) + k * 8 + t4;
+            const uint32_t* q1 = q0 + 8 * (R / 2);
+            qb[k][0] = grp < rows ? __ldg(q0) : 0u;
+            qb[k][1] = grp < rows ? __ldg(q0 + 4) : 0u;
+            qb[k][2] = grp + 8 < rows ? __ldg(q1) : 0u;
+            qb[k][3] = grp + 8 < rows ? __ldg(q1 + 4) : 0u;
+          }
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int a = 8 * n + 2 * t4 + e;        // this lane's column
+              lse[n][e] = a < rows ? p.lse2[at0 + a] : 0.f;
+              pos[n][e] = a < rows ? cache_pos(it.x, (b * MT + a) / c.heads) : -1;
+            }
+        }
+        float s[2][4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+#pragma unroll
+        for (int k = 0; k < R / 16; ++k) {
+          uint32_t a[4];
+          ldsm4(kv_addr + (k >> 2) * C::KV_SUB + k_row + (((2 * (k & 3) + k_chunk) ^ xr) << 4), a);
+          mma16816(s[0], a, qb[k][0], qb[k][1]);
+          mma16816(s[1], a, qb[k][2], qb[k][3]);
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int32_t t = t0 + grp + 8 * (e >> 1), ps = pos[n][e & 1];
+            const bool see = t <= ps && (t >= cache_low(c, ps) || t < c.n_sink);
+            const float x = ex2_approx(fmaf(s[n][e], p.scale2, -lse[n][e & 1]));
+            sum[e >> 1] += see ? x : 0.f;
+          }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&kv_empty[st]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
+        sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
+        const int32_t t = t0 + grp + 8 * h;
+        if (t4 == 0 && cache_seen(c, it.k.all, t, t + 1)) {
+          const int64_t at = cache_row(c, c.table, c.stride, it.u, t);
+          if (at >= 0) atomicAdd(&p.mass[at], sum[h]);
+        }
+      }
+      ++g;
+    }
+  }
+}
+
+template <int R>
+cudaError_t launch_mass_r(const CacheAttn& a, const CUtensorMap& tmC, int num_sms, cudaStream_t s) {
+  using C = Cfg<R>;
+  static uint64_t attr_devices = 0;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (!(attr_devices >> (dev & 63) & 1)) {
+    cudaError_t e = cudaFuncSetAttribute(cache_mass_token_kernel<R>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+    if (e != cudaSuccess) return e;
+    attr_devices |= 1ull << (dev & 63);
+  }
+  return launch_dependent(cache_mass_token_kernel<R>, dim3(num_sms), dim3(kThreads), C::SMEM, s, 1,
+                          tmC, a);
+}
+
 template <int R>
 cudaError_t launch_r(CacheAttn a, const CUtensorMap& tmC, int num_sms, cudaStream_t s) {
   using C = Cfg<R>;
@@ -444,6 +613,16 @@ cudaError_t launch_cache_token(const CacheAttn& a, const CUtensorMap& tmC, int n
     case 64: return launch_r<64>(a, tmC, num_sms, s);
     case 128: return launch_r<128>(a, tmC, num_sms, s);
     case 256: return launch_r<256>(a, tmC, num_sms, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+cudaError_t launch_cache_mass_token(const CacheAttn& a, const CUtensorMap& tmC, int num_sms,
+                                    cudaStream_t s) {
+  switch (a.c.r) {
+    case 64: return launch_mass_r<64>(a, tmC, num_sms, s);
+    case 128: return launch_mass_r<128>(a, tmC, num_sms, s);
+    case 256: return launch_mass_r<256>(a, tmC, num_sms, s);
     default: return cudaErrorInvalidValue;
   }
 }
