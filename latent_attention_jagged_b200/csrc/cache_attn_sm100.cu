@@ -43,7 +43,7 @@ namespace {
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int KT = 128;                   // events of a tile
 constexpr int HT = KT / 2;                // events of a half
-constexpr int NG = 4;                     // softmax groups, half S buffers
+constexpr int NG = 4;                     // softmax groups
 
 // Six warpgroups: producer (warp 0), issuers of S (warp 1) and of P C (warp 2); four of
 // softmax; the epilogue.  The launch's 80 registers a thread are dealt out again: 128 threads x
@@ -62,9 +62,15 @@ template <int R, int MT>
 struct Cfg {
   static constexpr bool SMALL = MT == 32;
   static constexpr int RSUB = R / 64;
-  static constexpr int OBUF = (2 * R + NG * HT <= 512) ? 2 : 1;
+  // Half S buffers: 3 tiles where tensor memory has the room, so that a softmax group
+  // finds its next half ready (with 2 tiles it waits for S after P C of its last one)
+  static constexpr int NS = R == 64 ? 6 : 4;
+  static constexpr int OBUF = 2 * R + NS * HT <= 512 ? 2 : 1;
   static constexpr int QBUF = SMALL || R <= 128 ? 2 : 1;
-  static constexpr int KS = SMALL ? (R == 256 ? 6 : 12) : (R == 256 ? 4 : R == 128 ? 8 : 12);   // halves in the ring
+  static constexpr int KS = SMALL ? (R == 256 ? 6 : 12) : (R == 256 ? 4 : R == 128 ? 6 : 12);   // halves in the ring
+  // 32 rows x 64 columns of output on their way to global memory, for each quadrant
+  static constexpr int NSTG = SMALL ? 0 : R == 128 ? 2 : 1;
+  static constexpr uint32_t STG_BYTES = 32 * 128;
   static constexpr uint32_t QSUB = MT * 128;           // one 64-wide sub-tile of a query block
   static constexpr uint32_t Q_BYTES = RSUB * QSUB;
   // The ring: for each 64 columns KS halves of 64 rows, so that the halves of a tile
@@ -77,37 +83,15 @@ struct Cfg {
   static constexpr int NQ = SMALL ? 1 : 4;             // TMEM lane quadrants in use
   static constexpr uint32_t BAR_BYTES = R == 256 ? 512 : 576;
   static constexpr uint32_t F_BYTES = (OBUF * 2 + 1) * NG * MT * 4;   // sums, maxima
-  static constexpr size_t SMEM = 1024 + QBUF * Q_BYTES + (size_t)KS * H_BYTES + BAR_BYTES +
-                                 F_BYTES;
+  static constexpr size_t SMEM = 1024 + QBUF * Q_BYTES + (size_t)KS * H_BYTES +
+                                 4 * NSTG * STG_BYTES + BAR_BYTES + F_BYTES;
   static_assert(SMEM <= 232448, "shared memory budget");
-  static_assert(OBUF * R + NG * HT <= 512, "TMEM budget");
+  static_assert(OBUF * R + NS * HT <= 512, "TMEM budget");
   // an M = 128 product reads 16 KB from the start of a 32-row sub-tile
   static_assert(!SMALL || KS * H_BYTES >= 16384, "operand reads stay in the buffers");
   // the split works in the ring before its first load
   static_assert(KS * H_BYTES >= sizeof(CacheSplitSpace), "split");
 };
-
-// 2^x for two values on the FMA pipe: x = j + f with j = rint(x), 2^f from the
-// polynomial of degree 5 with the least maximum relative error on [-1/2, 1/2]
-// (7.5e-8; 2.1e-7 with fp32 rounding, 2^-22), j added to the exponent field.
-// x <= -125 gives 0, as a hidden score must; NaN stays NaN.
-__device__ __forceinline__ float2 exp2_fma(float2 x) {
-  constexpr float kRound = 12582912.f;  // 1.5 * 2^23: j in the low bits of the sum
-  auto two = [](float v) { return make_float2(v, v); };
-  const float2 t = add_f2(x, two(kRound));
-  const float2 f = fma_f2(add_f2(t, two(-kRound)), two(-1.f), x);
-  float2 e = fma_f2(two(0x1.5c08e6p-10f), f, two(0x1.3d0c52p-7f));
-  e = fma_f2(e, f, two(0x1.c6b6e4p-5f));
-  e = fma_f2(e, f, two(0x1.ebf918p-3f));
-  e = fma_f2(e, f, two(0x1.62e428p-1f));
-  e = fma_f2(e, f, two(0x1.000002p+0f));
-  float2 r;
-  r.x = __uint_as_float(__float_as_uint(e.x) + (__float_as_uint(t.x) << 23));
-  r.y = __uint_as_float(__float_as_uint(e.y) + (__float_as_uint(t.y) << 23));
-  r.x = x.x <= -125.f ? 0.f : x.x != x.x ? x.x : r.x;
-  r.y = x.y <= -125.f ? 0.f : x.y != x.y ? x.y : r.y;
-  return r;
-}
 
 // One warp clears the latents of half a tile that are not finite, so that a weight of
 // 0 hides them (several warps may do so at once: they write the same zeros).
@@ -147,30 +131,31 @@ __device__ __forceinline__ void put32(void* dst, bool wide, uint32_t a, uint32_t
 template <int R, int MT>
 __global__ void __launch_bounds__(kThreads, 1)
 cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmC,
-                  const CacheAttn p) {
+                  const __grid_constant__ CUtensorMap tmO, const CacheAttn p) {
   using C = Cfg<R, MT>;
   using Line = ByRows<MT, KT>;
-  constexpr int RSUB = C::RSUB, KS = C::KS, OBUF = C::OBUF, QBUF = C::QBUF;
+  constexpr int RSUB = C::RSUB, KS = C::KS, OBUF = C::OBUF, QBUF = C::QBUF, NS = C::NS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* sQ = smem;
   uint8_t* sKV = sQ + QBUF * C::Q_BYTES;
-  uint64_t* bars = (uint64_t*)(sKV + KS * C::H_BYTES);
+  uint8_t* sStage = sKV + KS * C::H_BYTES;                   // [4][NSTG] of STG_BYTES
+  uint64_t* bars = (uint64_t*)(sStage + 4 * C::NSTG * C::STG_BYTES);
   uint64_t* q_full = bars;                 // [2]
   uint64_t* q_empty = bars + 2;            // [2]
   uint64_t* o_full = bars + 4;             // [2] last P C done, sums and maxima written
   uint64_t* o_free = bars + 6;             // [2] the epilogue has read O
-  uint64_t* s_full = bars + 8;             // [2] by tile
-  uint64_t* p_full = bars + 12;            // [NG] every softmax warp of the group has written P
-  uint64_t* p_empty = bars + 16;           // [NG] P C done
-  uint64_t* m_full = bars + 20;            // [NG][4] a quadrant's maximum after a tile
-  uint64_t* kv_full = bars + 36;           // [KS]
+  uint64_t* s_full = bars + 8;             // [NS / 2] by tile
+  uint64_t* p_full = bars + 11;            // [NS] every softmax warp of the group has written P
+  uint64_t* p_empty = bars + 17;           // [NS] P C done
+  uint64_t* m_full = bars + 23;            // [NG][4] a quadrant's maximum after a half
+  uint64_t* kv_full = bars + 39;           // [KS]
   uint64_t* kv_empty = kv_full + KS;       // [KS]
   uint64_t* drain = kv_empty + KS;
   uint32_t* tmem_slot = (uint32_t*)(drain + 2);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   CacheSplit* split = (CacheSplit*)(tmem_slot + 2);
-  static_assert((36 + 2 * KS + 2) * 8 + 8 + sizeof(CacheSplit) <= C::BAR_BYTES, "barriers");
+  static_assert((39 + 2 * KS + 2) * 8 + 8 + sizeof(CacheSplit) <= C::BAR_BYTES, "barriers");
   // of every row: by O buffer and group a sum and its base, by group the maximum so far
   float* lbuf = (float*)((uint8_t*)bars + C::BAR_BYTES);     // [OBUF][NG][MT]
   float* mbuf = lbuf + OBUF * NG * MT;                       // [OBUF][NG][MT]
@@ -187,11 +172,13 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       mbar_init(&q_empty[s], 1);
       mbar_init(&o_full[s], 1 + NG * C::NQ);
       mbar_init(&o_free[s], C::NQ);
-      mbar_init(&s_full[s], 1);
     }
-    for (int s = 0; s < NG; ++s) {
+    for (int s = 0; s < NS / 2; ++s) mbar_init(&s_full[s], 1);
+    for (int s = 0; s < NS; ++s) {
       mbar_init(&p_full[s], C::NQ);
       mbar_init(&p_empty[s], 1);
+    }
+    for (int s = 0; s < NG; ++s) {
       for (int q = 0; q < 4; ++q) mbar_init(&m_full[s * 4 + q], 1);
     }
     for (int s = 0; s < KS; ++s) { mbar_init(&kv_full[s], 1); mbar_init(&kv_empty[s], 1); }
@@ -201,6 +188,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     fence_mbar_init();
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmC);
+    tma_prefetch_desc(&tmO);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, 512);
@@ -304,11 +292,11 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       if (!warp_wait(&q_full[qb], (itm / QBUF) & 1, abort_flag, c.status)) break;
       const uint64_t ad = sdesc_sw128(smem_u32(sQ + qb * C::Q_BYTES), 16, 1024);
       for (int i = it.t0; i < it.t1; ++i, ++g) {
-        const int st = (2 * g) % KS, sb = g & 1;
+        const int st = (2 * g) % KS, sb = g % (NS / 2);
         // both halves are here; the products that read P in this S buffer are done
         ok = warp_wait(&kv_full[st], (2 * g / KS) & 1, abort_flag, c.status) &&
              warp_wait(&kv_full[st + 1], (2 * g / KS) & 1, abort_flag, c.status) &&
-             warp_wait(&p_empty[2 * sb + 1], ((g >> 1) & 1) ^ 1, abort_flag, c.status);
+             warp_wait(&p_empty[2 * sb + 1], ((g / (NS / 2)) & 1) ^ 1, abort_flag, c.status);
         if (!ok) break;
         tc_fence_after();
         const uint64_t bd = sdesc_sw128(smem_u32(sKV + st * C::H_SUB), 16, 1024);
@@ -346,8 +334,8 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       const int ob = itm % OBUF;
       if (!warp_wait(&o_free[ob], ((itm / OBUF) & 1) ^ 1, abort_flag, c.status)) break;
       for (int i = 2 * it.t0; i < 2 * it.t1; ++i, ++g) {
-        const int st = g % KS, sb = g % NG;
-        ok = warp_wait(&p_full[sb], (g / NG) & 1, abort_flag, c.status);
+        const int st = g % KS, sb = g % NS;
+        ok = warp_wait(&p_full[sb], (g / NS) & 1, abort_flag, c.status);
         if (!ok) break;
         tc_fence_after();
         const uint64_t bd = sdesc_sw128(smem_u32(sKV + st * C::H_SUB), C::KV_SUB, 1024);
@@ -375,13 +363,12 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   } else if (warp < 20) {
   if (quad < C::NQ) {
     // ------------------------------------------------------------ softmax
-    // The groups take the halves in turn, group g % NG half g with S buffer g % NG; a
-    // thread owns a row.  Only the running maximum goes from one group to the next,
+    // The groups take the halves in turn, group g % NG half g; a thread owns a
+    // row.  Only the running maximum goes from one group to the next,
     // as soon as it is known, so that the latencies of NG halves overlap.
     const int group = (warp >> 2) - 1, before = (group + NG - 1) % NG;
     const int row = quad * 32 + lane;                  // pair in the block = TMEM lane
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
-    const uint32_t s_addr = lane_base + C::S_COL + group * HT;
     const float mul = p.scale2 == 0.f ? 1.f : fabsf(p.scale2);
     const float2 mul2 = make_float2(mul, mul);
     uint32_t g = 0, itm = 0;
@@ -403,7 +390,9 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       bool poison = false;
       for (int i = 2 * it.t0; i < 2 * it.t1; ++i, ++g) {
         if ((int)(g % NG) != group) continue;
-        bool w = mbar_wait(&s_full[group >> 1], (g / NG) & 1, abort_flag, c.status);
+        const int sb = g % NS;
+        const uint32_t s_addr = lane_base + C::S_COL + sb * HT;
+        bool w = mbar_wait(&s_full[sb >> 1], (g / NS) & 1, abort_flag, c.status);
         if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
         tc_fence_after();
         float mt = -INFINITY;
@@ -444,7 +433,10 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                   }
                 }
               }
-              if (masked) {
+              if (masked && sk >= lo) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) v[k] = k < hi ? v[k] : -INFINITY;
+              } else if (masked) {
 #pragma unroll
                 for (int k = 0; k < 32; ++k) v[k] = (vis >> k) & 1 ? v[k] : -INFINITY;
               }
@@ -466,19 +458,19 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
           if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
         }
         const float m_prev = i == 2 * it.t0 ? -INFINITY : mrow[before * MT + row];
-        // O and the sums keep their base until the maximum grows by more than 2^8
-        const bool resc = i > 2 * it.t0 && mt > m_prev + 8.f;
+        // O and the sums keep their base until the maximum grows by more than kGrow
+        const bool resc = i > 2 * it.t0 && mt > m_prev + kGrow;
         const float m_now = i == 2 * it.t0 || resc ? mt : m_prev;
         mrow[group * MT + row] = m_now;
         __syncwarp();
         if (lane == 0) mbar_arrive(&m_full[group * 4 + quad]);
         if (idle) {
-          if (lane == 0) mbar_arrive(&p_full[group]);
+          if (lane == 0) mbar_arrive(&p_full[sb]);
           continue;
         }
         if (__any_sync(0xffffffffu, resc)) {
           // the previous product must be in O: the next phase of its p_empty
-          w = mbar_wait(&p_empty[before], ((g - 1) / NG) & 1, abort_flag, c.status);
+          w = mbar_wait(&p_empty[(g - 1) % NS], ((g - 1) / NS) & 1, abort_flag, c.status);
           if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
           tc_fence_after();
           const float scale = resc ? ex2_approx(m_prev - m_now) : 1.f;
@@ -492,9 +484,9 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
           }
         }
         // weights 2^(s - m), the sum in fp32 of the unrounded ones; a row that has
-        // seen nothing yet subtracts 0 from its -inf.  One pair in four takes the
-        // FMA pipe: the special-function unit's 4 exponentials a cycle and scheduler
-        // would cost a tile 512 cycles.
+        // seen nothing yet subtracts 0 from its -inf.  All of them take the special-
+        // function unit (512 cycles a half and scheduler): a polynomial on the FMA pipe
+        // for one pair in four cost more issue slots than it saved.
         const float m_use = m_now > -INFINITY ? m_now : 0.f;
         const float2 nm2 = make_float2(-m_use, -m_use);
         float2 l4[2];
@@ -508,12 +500,8 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             float2 x = fma_f2(make_float2(v[2 * k], v[2 * k + 1]), mul2, nm2);
-            if ((k & 3) == 3) {
-              x = exp2_fma(x);
-            } else {
-              x.x = ex2_approx(x.x);
-              x.y = ex2_approx(x.y);
-            }
+            x.x = ex2_approx(x.x);
+            x.y = ex2_approx(x.y);
             l4[k & 1] = add_f2(l4[k & 1], x);
             pk[k] = pack_bf16(x.x, x.y);
           }
@@ -522,7 +510,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[group]);
+        if (lane == 0) mbar_arrive(&p_full[sb]);
         // the sum's base follows the maximum (also past changes of the other groups);
         // -inf: no sum yet
         if (m_now != m_run) {
@@ -554,7 +542,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     CacheJoin* join = p.join + blockIdx.x;
     const bool writer = warp == 20 && lane == 0;
     if (writer) join->rows = 0;
-    uint32_t itm = 0;
+    uint32_t itm = 0, stg = 0;             // items, staged boxes
     CacheItems<Line> items;
     items.start(c, run);
     CacheItem<Line> it;
@@ -562,6 +550,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       const uint32_t pairs = (uint32_t)it.x.n * (uint32_t)c.heads;
       const uint32_t pair = (uint32_t)it.b * MT + row;
       const bool valid = pair < pairs;
+      const bool box = C::NSTG > 0 && (uint32_t)it.b * MT + quad * 32 + 32 <= pairs;
       const bool idle = (uint32_t)it.b * MT + quad * 32 >= pairs;
       const int64_t at = it.x.row0 * c.heads + pair;
       __nv_bfloat16* orow = (__nv_bfloat16*)p.out + at * R;
@@ -589,8 +578,40 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         const uint32_t o_addr = lane_base + ob * R;
         if (it.whole) {
           const float inv = l != 0.f ? 1.f / l : 0.f;
+          if (box) {
+            // all 32 rows are the user's: they leave as boxes, so that O is free as soon
+            // as it has been read (64 stores of a lane's own row cost 3500 cycles)
 #pragma unroll 1
-          for (int k = 0; k < R; k += 32) {
+            for (int k = 0; k < R; k += 64, ++stg) {
+              uint8_t* buf = sStage + (quad * C::NSTG + stg % max(C::NSTG, 1)) * C::STG_BYTES;
+              if (lane == 0)
+                asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(C::NSTG > 0 ? C::NSTG - 1 : 0)
+                             : "memory");
+              __syncwarp();
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                float v[32];
+                tmem_ld32(o_addr + k + 32 * h, v);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const float* e = v + 8 * j;
+                  st_shared_v4(smem_u32(buf) + lane * 128 + (((4 * h + j) ^ (lane & 7)) << 4),
+                               make_uint4(pack_bf16(e[0] * inv, e[1] * inv),
+                                          pack_bf16(e[2] * inv, e[3] * inv),
+                                          pack_bf16(e[4] * inv, e[5] * inv),
+                                          pack_bf16(e[6] * inv, e[7] * inv)));
+                }
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                tma_store_2d(&tmO, smem_u32(buf), k, (int32_t)(at - lane));
+                tma_store_commit();
+              }
+            }
+          }
+#pragma unroll 1
+          for (int k = box ? R : 0; k < R; k += 32) {
             float v[32];
             tmem_ld32(o_addr + k, v);
             uint32_t x[16];
@@ -635,6 +656,8 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       }
       ++itm;
     }
+    if (lane == 0) tma_store_wait_all();
+    __syncwarp();
   }
   }
   __syncthreads();
@@ -714,11 +737,12 @@ cudaError_t launch_rm(const CacheAttn& a, const CUtensorMap& tmC, int num_sms, c
     if (f.numRegs * 6 < kRegsIssue + NG * kRegsSoft + kRegsEpi) return cudaErrorInvalidConfiguration;
     attr_devices |= 1ull << (dev & 63);
   }
-  CUtensorMap tmQ;
-  if (!make_tmap_bf16(&tmQ, a.q, (uint64_t)a.c.rows * a.c.heads, R, MT))
+  CUtensorMap tmQ, tmO;
+  const uint64_t pairs = (uint64_t)a.c.rows * a.c.heads;
+  if (!make_tmap_bf16(&tmQ, a.q, pairs, R, MT) || !make_tmap_bf16(&tmO, a.out, pairs, R, 32))
     return cudaErrorInvalidValue;
   cudaError_t e = launch_dependent(cache_attn_kernel<R, MT>, dim3(num_sms), dim3(kThreads),
-                                   C::SMEM, s, 1, tmQ, tmC, a);
+                                   C::SMEM, s, 1, tmQ, tmC, tmO, a);
   if (e != cudaSuccess) return e;
   return a.never_cut ? cudaSuccess : launch_cache_join(a, MT, num_sms, s);
 }

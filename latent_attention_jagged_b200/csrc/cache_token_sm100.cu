@@ -285,7 +285,7 @@ cache_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn p) {
           if (__any_sync(0xffffffffu, odd)) clear_rows<R>(kv, warp * 16);
         }
         // running maxima; O and the sums keep their base until one grows by more than
-        // 2^8 (a row that has seen nothing yet takes the first maximum it meets)
+        // kGrow (a row that has seen nothing yet takes the first maximum it meets)
         float mt[2];
         bool grow = false;
 #pragma unroll
@@ -293,7 +293,7 @@ cache_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn p) {
           mt[h] = fmaxf(fmaxf(v[0][2 * h], v[0][2 * h + 1]), fmaxf(v[1][2 * h], v[1][2 * h + 1]));
           mt[h] = fmaxf(mt[h], __shfl_xor_sync(0xffffffffu, mt[h], 1));
           mt[h] = fmaxf(mt[h], __shfl_xor_sync(0xffffffffu, mt[h], 2));
-          grow |= mt[h] > m[h] + 8.f;
+          grow |= mt[h] > m[h] + kGrow;
         }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
