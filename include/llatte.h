@@ -587,6 +587,34 @@ typedef struct {
 int llatte_cache_evict(llatte_cache* cache, const llatte_cache_view* view,
                        const llatte_cache_evict_args* args, void* stream);
 
+/*
+ * A forward pass over cached histories: `batch` holds only the new events of
+ * every user (and the query tokens), and each layer appends its latents of them
+ * to its cache and attends over that.  For a model whose layers keep every row
+ * (keep[l] >= max_len in every layer) the result is llatte_forward's on the whole
+ * histories; after eviction, or with a window, it is the attention over what is
+ * left.  The context must be the one the cached events were computed with.
+ *   caches      host array [n_layers], one cache per layer, of the handle's heads,
+ *               rank and dtype, with max_rows >= the handle's query rows
+ *               (min(max_total or max_batch * max_len, max_batch * keep[0])
+ *               + max_batch * n_q)
+ *   views       host array [n_layers]; lengths count the new events.  Layers may
+ *               name the same table and lengths: their pools are apart
+ *   window, n_sink, accumulate   as in llatte_cache_attn
+ * LLATTE_ERR_UNSUPPORTED for a handle with a layer in MLA's per-head form (create it
+ * with LLATTE_ATTN_ABSORBED), with d_time > 0 (the code of an event changes with the
+ * request), with d_out > 0 (the mean is over rows that are not computed again),
+ * or whose layers drop rows.  Faults in the caches' arguments go to their own
+ * status words.  Asynchronous on `stream`.
+ */
+typedef struct {
+  llatte_cache* const* caches;
+  const llatte_cache_view* views;
+  int32_t window, n_sink, accumulate;
+} llatte_forward_cache;
+int llatte_forward_cached(llatte_handle* handle, const llatte_batch* batch,
+                          const llatte_forward_cache* cache, float* out, void* stream);
+
 /* Synchronise the device, read the status word and clear it (as
  * llatte_get_status does for a forward handle). */
 int llatte_cache_get_status(llatte_cache* cache, int32_t* device_status);

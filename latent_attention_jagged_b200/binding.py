@@ -106,6 +106,12 @@ class llatte_cache_evict_args(ctypes.Structure):
                 ("kept", ctypes.c_void_p)]
 
 
+class llatte_forward_cache(ctypes.Structure):
+    _fields_ = [("caches", ctypes.POINTER(ctypes.c_void_p)),
+                ("views", ctypes.POINTER(llatte_cache_view)), ("window", ctypes.c_int32),
+                ("n_sink", ctypes.c_int32), ("accumulate", ctypes.c_int32)]
+
+
 EXPORTS = ("llatte_create", "llatte_forward", "llatte_plan_export", "llatte_get_status",
            "llatte_workspace_bytes", "llatte_error_string", "llatte_destroy",
            "llatte_set_profiling", "llatte_profile_reset", "llatte_profile_step",
@@ -115,7 +121,7 @@ EXPORTS = ("llatte_create", "llatte_forward", "llatte_plan_export", "llatte_get_
            "llatte_tokenizer_destroy", "llatte_inject_timeout", "llatte_cache_workspace_bytes",
            "llatte_cache_create", "llatte_cache_append", "llatte_cache_attend",
            "llatte_cache_evict", "llatte_cache_get_status", "llatte_cache_uses_tensor_cores",
-           "llatte_cache_destroy")
+           "llatte_cache_destroy", "llatte_forward_cached")
 TOK_MAX_FIELDS = 8
 PLAN_STATIC_MAX_BATCH = 4096
 
@@ -195,6 +201,8 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.llatte_cache_uses_tensor_cores.restype = ctypes.c_int
     lib.llatte_cache_destroy.argtypes = [VP]
     lib.llatte_cache_destroy.restype = None
+    lib.llatte_forward_cached.argtypes = [VP, P(llatte_batch), P(llatte_forward_cache), VP, VP]
+    lib.llatte_forward_cached.restype = ctypes.c_int
     if path is None:
         _lib = lib
     return lib
@@ -409,6 +417,47 @@ class Llatte:
         self._run(values, offsets, context, cand,
                   event_age if getattr(d, "d_time", 0) else None, out, ex, stream, B)
         return out, recent, topk, hours
+
+    def query_rows(self) -> int:
+        """Most query rows of a call: the max_rows a cache of forward_cached needs."""
+        c = self.cdims
+        rows = int(c.max_total) or int(c.max_batch) * int(c.max_len)
+        return min(rows, int(c.max_batch) * int(c.keep[0])) + int(c.max_batch) * int(c.n_q)
+
+    def forward_cached(self, values: torch.Tensor, offsets: torch.Tensor,
+                       caches: Sequence["LatentCache"], tables, lengths: torch.Tensor,
+                       context=None, cand=None, window: int = 0, n_sink: int = 0,
+                       accumulate: bool = False, out: Optional[torch.Tensor] = None,
+                       stream=None) -> torch.Tensor:
+        """A forward pass whose `values` are only the new events of every user: layer l
+        appends their latents to caches[l] and attends over it.  tables: one page
+        table, or one per layer; lengths: cached events, the new ones included.
+        The layers must keep every row (see llatte_forward_cached)."""
+        if getattr(self.dims, "d_time", 0):      # the code of an event changes with the request
+            raise LlatteError(LLATTE_ERR_UNSUPPORTED, "llatte_forward_cached")
+        B = self._check_inputs(values, offsets, context, cand, None)
+        n = len(self.dims.keep)
+        if len(caches) != n:
+            raise ValueError("one cache per layer is required")
+        if isinstance(tables, torch.Tensor):
+            tables = [tables] * n
+        if len(tables) != n:
+            raise ValueError("one page table, or one per layer, is required")
+        handles = (ctypes.c_void_p * n)(*[c.h for c in caches])
+        views = (llatte_cache_view * n)(*[c._view(t, lengths)[0] for c, t in zip(caches, tables)])
+        if any(v.B != B for v in views):
+            raise ValueError(f"tables and lengths must have {B} users")
+        out = self._out(out, B, values.device)
+        b = llatte_batch(values=values.data_ptr(), offsets=offsets.data_ptr(), B=B,
+                         context=context.data_ptr() if context is not None else None,
+                         cand=cand.data_ptr() if cand is not None else None, event_age=None)
+        fc = llatte_forward_cache(handles, views, int(window), int(n_sink), 1 if accumulate else 0)
+        rc = self.lib.llatte_forward_cached(self.h, ctypes.byref(b), ctypes.byref(fc), _ptr(out),
+                                            _stream_ptr(stream))
+        if rc != LLATTE_OK:
+            raise LlatteError(rc, "llatte_forward_cached")
+        self.last_B = B
+        return out
 
     def plan_export(self, stream=None) -> torch.Tensor:
         L, B = len(self.dims.keep), self.last_B

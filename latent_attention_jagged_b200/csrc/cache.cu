@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(256) cache_append_kernel(CacheAppend a) {
   // the search below may pass by a faulty user: the last block looks at them all
   if (blockIdx.x == gridDim.x - 1)
     for (int u = threadIdx.x; u < c.B; u += 256) cache_user(c, u);
-  if (row0 >= c.rows) return;
+  if (row0 >= min(c.rows, __ldg(c.qoff + c.B))) return;
   const int nvec = c.r / EV, sub = lane / G, k0 = lane % G;
   uint4 v[4][NV];
 #pragma unroll
@@ -560,7 +560,57 @@ CacheCall make_call(const llatte_cache* h, const llatte_cache_view* v, const int
   return c;
 }
 
+CacheAttn make_attn(const llatte_cache* h, const llatte_cache_view* v, const void* q,
+                    const int64_t* qoff, int64_t rows, void* out) {
+  CacheAttn a = {};
+  a.c = make_call(h, v, qoff, rows);
+  a.pool = h->pool; a.mass = h->mass; a.q = q; a.out = out;
+  a.part_o = h->part_o; a.part_ml = h->part_ml; a.join = h->join;
+  return a;
+}
+
+// The attention, and the accumulation when a.lse2 is set.
+cudaError_t run_attn(llatte_cache* h, const CacheAttn& a, cudaStream_t s) {
+  const cudaError_t e = h->tc ? launch_cache_attn_tc(a, h->tmC, h->num_sms, s)
+                              : launch_cache_attn_simt(h->elem, a, h->num_sms, s);
+  if (e != cudaSuccess || !a.lse2) return e;
+  return h->tc ? launch_cache_mass_tc(a, h->tmC, h->num_sms, s)
+               : launch_cache_mass_simt(h->elem, a, h->num_sms, s);
+}
+
 }  // namespace
+
+namespace llatte {
+
+int cache_layer_check(const llatte_cache* h, const llatte_cache_view* v, int heads, int rank,
+                      int dtype, int64_t rows_q, int accumulate) {
+  const int rc = check_view(h, v);
+  if (rc != LLATTE_OK) return rc;
+  if (h->dims.heads != heads || h->dims.rank != rank || h->dims.dtype != dtype ||
+      h->dims.max_rows < rows_q || (accumulate && !h->mass))
+    return LLATTE_ERR_ARG;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return LLATTE_ERR_CUDA;
+  return dev == h->device ? LLATTE_OK : LLATTE_ERR_ARG;
+}
+
+int cache_layer_run(llatte_cache* h, const llatte_cache_view* v, const CacheLayer& l,
+                    cudaStream_t s) {
+  if (l.rows_h > 0) {
+    CacheAppend ap = {};
+    ap.c = make_call(h, v, l.hoff, l.rows_h);
+    ap.pool = h->pool; ap.mass = h->mass; ap.x = l.C;
+    if (launch_cache_append(h->elem, ap, s) != cudaSuccess) return LLATTE_ERR_CUDA;
+  }
+  CacheAttn a = make_attn(h, v, l.q, l.qoff, l.rows_q, l.out);
+  a.c.n_cand = l.n_cand; a.c.window = l.window; a.c.n_sink = l.n_sink;
+  a.lse2 = l.accumulate ? h->lse2 : nullptr;
+  a.scale2 = l.scale2;
+  a.pairs = l.pairs;
+  return run_attn(h, a, s) == cudaSuccess ? LLATTE_OK : LLATTE_ERR_CUDA;
+}
+
+}  // namespace llatte
 
 extern "C" {
 
@@ -660,22 +710,12 @@ int llatte_cache_attend(llatte_cache* h, const llatte_cache_view* v, const llatt
     return LLATTE_ERR_ARG;
   DeviceGuard g(h->device);
   if (!g.ok) return LLATTE_ERR_CUDA;
-  CacheAttn a = {};
-  a.c = make_call(h, v, p->q_offsets, p->rows);
+  CacheAttn a = make_attn(h, v, p->q, p->q_offsets, p->rows, p->out);
   a.c.n_cand = p->n_cand; a.c.window = p->window; a.c.n_sink = p->n_sink;
-  a.pool = h->pool; a.mass = h->mass; a.q = p->q; a.out = p->out; a.lse = p->lse;
-  a.lse2 = p->accumulate ? h->lse2 : nullptr;
+  a.lse = p->lse; a.lse2 = p->accumulate ? h->lse2 : nullptr;
   a.scale2 = p->scale * kLog2e;
-  cudaStream_t s = (cudaStream_t)stream;
-  a.part_o = h->part_o; a.part_ml = h->part_ml; a.join = h->join;
-  const cudaError_t e = h->tc ? launch_cache_attn_tc(a, h->tmC, h->num_sms, s)
-                              : launch_cache_attn_simt(h->elem, a, h->num_sms, s);
-  if (e != cudaSuccess) return LLATTE_ERR_CUDA;
-  if (!p->accumulate) return LLATTE_OK;
-  const cudaError_t m = h->tc ? launch_cache_mass_tc(a, h->tmC, h->num_sms, s)
-                              : launch_cache_mass_simt(h->elem, a, h->num_sms, s);
-  if (m != cudaSuccess) return LLATTE_ERR_CUDA;
-  return LLATTE_OK;
+  a.pairs = p->rows * h->dims.heads;
+  return run_attn(h, a, (cudaStream_t)stream) == cudaSuccess ? LLATTE_OK : LLATTE_ERR_CUDA;
 }
 
 int llatte_cache_evict(llatte_cache* h, const llatte_cache_view* v,

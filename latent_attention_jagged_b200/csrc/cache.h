@@ -43,10 +43,26 @@ struct CacheAttn {
   float* part_o;             // [2 CTAs, block rows, r] unnormalised sums
   float2* part_ml;           // [2 CTAs, block rows] maximum (log2 units) and sum
   CacheJoin* join;           // [CTAs]
+  int64_t pairs;             // (row, head) pairs of the call, as far as the host can tell
   int32_t min_quota;         // fewest tiles of a CTA's run
   bool never_cut;            // no block is cut between CTAs (then there is nothing to join)
   float scale2;              // scale * log2(e): scores in log2 units
 };
+
+// One layer of a forward pass over a cache (llatte_forward_cached): appends the latents
+// C of the new events, then attends with the queries q of its rows.
+struct CacheLayer {
+  const void* C; const int64_t* hoff; int64_t rows_h;    // [rows_h, r], user offsets
+  const void* q; const int64_t* qoff; int64_t rows_q;    // [rows_q, h, r]
+  void* out;
+  int64_t pairs;             // estimate of the pairs in use
+  int32_t n_cand, window, n_sink, accumulate;
+  float scale2;              // scores in log2 units = scale2 * q . c
+};
+int cache_layer_check(const llatte_cache* h, const llatte_cache_view* v, int heads, int rank,
+                      int dtype, int64_t rows_q, int accumulate);
+int cache_layer_run(llatte_cache* h, const llatte_cache_view* v, const CacheLayer& a,
+                    cudaStream_t s);
 
 struct CacheAppend {
   CacheCall c;

@@ -754,7 +754,7 @@ cudaError_t launch_r(CacheAttn a, const CUtensorMap& tmC, int num_sms, cudaStrea
   a.min_quota = 1;
   a.never_cut = cache_most_tiles(a.c, 128, KT) <= 4;
   // few pairs a user on average: see cache_token_sm100.cu
-  if (a.c.rows * a.c.heads <= 16 * (int64_t)a.c.B) return launch_cache_token(a, tmC, num_sms, s);
+  if (a.pairs <= 16 * (int64_t)a.c.B) return launch_cache_token(a, tmC, num_sms, s);
 
   return launch_rm<R, 128>(a, tmC, num_sms, s);
 }

@@ -369,7 +369,7 @@ cudaError_t launch_rn(const CacheAttn& a, const CUtensorMap& tmC, int num_sms, c
 
 template <int R>
 cudaError_t launch_r(const CacheAttn& a, const CUtensorMap& tmC, int num_sms, cudaStream_t s) {
-  if (a.c.rows * a.c.heads <= 16 * (int64_t)a.c.B)
+  if (a.pairs <= 16 * (int64_t)a.c.B)
     return launch_cache_mass_token(a, tmC, num_sms, s);
   return launch_rn<R, 128>(a, tmC, num_sms, s);
 }

@@ -657,11 +657,10 @@ cudaError_t launch_with(K kernel, int grid, int threads, size_t smem, const Cach
 template <typename T>
 cudaError_t attn_t(CacheAttn a, int num_sms, cudaStream_t s) {
   const int r = a.c.r, pitch = r + 16 / (int)sizeof(T);
-  const int64_t pairs = a.c.rows * a.c.heads;
   a.min_quota = 1;
   int mt;
   cudaError_t e;
-  if (pairs <= TP * (int64_t)a.c.B) {
+  if (a.pairs <= TP * (int64_t)a.c.B) {
     mt = TP;
     // as many warps as two tiles of each leave room for
     const size_t warp = 2 * TK * pitch * sizeof(T) + TP * TK * 4;

@@ -6,6 +6,7 @@
 #include <algorithm>
 #include <new>
 
+#include "cache.h"
 #include "internal.h"
 #include "tc_attn.h"
 #include "tc_ffn.h"
@@ -635,7 +636,7 @@ int check_export(const llatte_handle* h, const llatte_attn_export* ex) {
 
 int forward_impl(llatte_handle* h, const void* values, const int64_t* offsets, int32_t B,
                  const void* context, const void* cand, const float* ages, float* out,
-                 void* stream) {
+                 void* stream, const llatte_forward_cache* fc = nullptr) {
   const llatte_dims& D = h->dims;
   if (B < 0 || B > D.max_batch) return LLATTE_ERR_ARG;
   if (B == 0) { h->last_B = 0; return LLATTE_OK; }
@@ -850,7 +851,19 @@ int forward_impl(llatte_handle* h, const void* values, const int64_t* offsets, i
       }
       if (!rq) t.done(1);
     }
-    if (tc) {  // latent attention, tensor cores
+    if (fc) {  // latent attention over the layer's cache, the new events appended
+      StepTimer t(h, s, ST_ATTN);
+      CacheLayer a = {};
+      a.C = h->C; a.hoff = p.hoff(l); a.rows_h = h->max_rows_h;
+      a.q = h->Qt; a.qoff = p.qoff(l); a.rows_q = h->max_rows_q; a.out = h->Ot;
+      a.pairs = (h->max_rows_q + D.max_batch - 1) / D.max_batch * B * D.heads;
+      a.n_cand = D.n_q; a.window = fc->window; a.n_sink = fc->n_sink;
+      a.accumulate = fc->accumulate;
+      a.scale2 = tc ? 1.f : 1.4426950408889634f;   // log2 e is folded into the tensor-core q~
+      const int rc = cache_layer_run(fc->caches[l], &fc->views[l], a, s);
+      if (rc != LLATTE_OK) return rc;
+      t.done(fc->accumulate ? 5 : 3);
+    } else if (tc) {  // latent attention, tensor cores
       StepTimer t(h, s, ST_ATTN);
       AttnTcParams a = {};
       a.work = p.work + (int64_t)l * 2 * p.max_work; a.work_count = p.work_count + l;
@@ -1048,6 +1061,24 @@ int llatte_forward_batch(llatte_handle* h, const llatte_batch* b, float* out,
                               h->dims.d_time > 0 ? b->event_age : nullptr, out, stream);
   h->export_req = nullptr;
   return rc;
+}
+
+int llatte_forward_cached(llatte_handle* h, const llatte_batch* b, const llatte_forward_cache* fc,
+                          float* out, void* stream) {
+  if (!h || !b || !fc || !fc->caches || !fc->views) return LLATTE_ERR_ARG;
+  const llatte_dims& D = h->dims;
+  if (fc->window < 0 || fc->n_sink < 0 || (fc->accumulate != 0 && fc->accumulate != 1))
+    return LLATTE_ERR_ARG;
+  if (h->heads_mask != 0 || D.d_time > 0 || D.d_out > 0) return LLATTE_ERR_UNSUPPORTED;
+  for (int l = 0; l < D.n_layers; ++l) {
+    if (D.keep[l] < D.max_len) return LLATTE_ERR_UNSUPPORTED;
+    const llatte_cache_view* v = &fc->views[l];
+    if (v->B != b->B) return LLATTE_ERR_ARG;
+    const int rc = cache_layer_check(fc->caches[l], v, D.heads, D.rank, D.dtype, h->max_rows_q,
+                                     fc->accumulate);
+    if (rc != LLATTE_OK) return rc;
+  }
+  return forward_impl(h, b->values, b->offsets, b->B, b->context, b->cand, nullptr, out, stream, fc);
 }
 
 int llatte_plan_export(llatte_handle* h, int64_t* dst, void* stream) {
