@@ -45,8 +45,8 @@ constexpr int KT = 128;                   // events of a tile
 constexpr int HT = KT / 2;                // events of a half
 constexpr int NG = 4;                     // softmax groups
 
-// Six warpgroups: producer (warp 0), issuers of S (warp 1) and of P C (warp 2); four of
-// softmax; the epilogue.  The launch's 80 registers a thread are dealt out again: 128 threads x
+// Six warpgroups: producer (warp 0), issuers of S (warp 1) and of P C (warp 2), the
+// planner (warp 3); four of softmax; the epilogue.  The launch's 80 registers a thread are dealt out again: 128 threads x
 // (56 + 4 x 80 + 104) = 768 x 80 (softmax keeps what it has).
 constexpr int kThreads = 768;
 constexpr int kRegsIssue = 56, kRegsSoft = 80, kRegsEpi = 104;
@@ -57,6 +57,22 @@ template <int N> __device__ __forceinline__ void regs_up() {
 template <int N> __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
+
+// What the roles have to know about a piece of work.  One warp walks the CTA's run and
+// hands the pieces round in a ring: with the walk in every role the kernel's code did
+// not fit the instruction cache, and short pieces spent their time fetching it (64
+// candidates for 256 users: 44 us).
+struct __align__(16) Piece {
+  int64_t at0;               // first (row, head) pair, in the call's rows
+  int32_t u;                 // user (-1: the run is over)
+  int32_t pair0, rows;       // the block's first pair in the user's, and its pairs
+  int32_t m, len;            // the user's new events and cached events
+  int32_t t0, t1;            // tiles of the piece
+  CacheBlock k;
+  int32_t parts;             // CTAs that share the block
+  int32_t whole, starts;
+};
+constexpr int NPIECE = 4;
 
 template <int R, int MT>
 struct Cfg {
@@ -81,7 +97,7 @@ struct Cfg {
   static_assert(KS % 2 == 0 && KS >= NG, "halves of a tile are neighbours");
   static constexpr uint32_t S_COL = OBUF * R;
   static constexpr int NQ = SMALL ? 1 : 4;             // TMEM lane quadrants in use
-  static constexpr uint32_t BAR_BYTES = R == 256 ? 512 : 576;
+  static constexpr uint32_t BAR_BYTES = 576 + NPIECE * (sizeof(Piece) + 16);
   static constexpr uint32_t F_BYTES = (OBUF * 2 + 1) * NG * MT * 4;   // sums, maxima
   static constexpr size_t SMEM = 1024 + QBUF * Q_BYTES + (size_t)KS * H_BYTES +
                                  4 * NSTG * STG_BYTES + BAR_BYTES + F_BYTES;
@@ -92,6 +108,21 @@ struct Cfg {
   // the split works in the ring before its first load
   static_assert(KS * H_BYTES >= sizeof(CacheSplitSpace), "split");
 };
+
+// One column of this lane's row.
+__device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  asm volatile("" : "+r"(r));
+  return __uint_as_float(r);
+}
+__device__ __forceinline__ void tmem_st1(uint32_t taddr, float v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr),
+               "r"(__float_as_uint(v))
+               : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
 
 // One warp clears the latents of half a tile that are not finite, so that a weight of
 // 0 hides them (several warps may do so at once: they write the same zeros).
@@ -155,7 +186,10 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   uint32_t* tmem_slot = (uint32_t*)(drain + 2);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   CacheSplit* split = (CacheSplit*)(tmem_slot + 2);
-  static_assert((39 + 2 * KS + 2) * 8 + 8 + sizeof(CacheSplit) <= C::BAR_BYTES, "barriers");
+  uint64_t* piece_full = (uint64_t*)((uint8_t*)bars + 576);  // [NPIECE]
+  uint64_t* piece_empty = piece_full + NPIECE;               // [NPIECE]
+  Piece* pieces = (Piece*)(piece_empty + NPIECE);
+  static_assert((39 + 2 * KS + 2) * 8 + 8 + sizeof(CacheSplit) <= 576, "barriers");
   // of every row: by O buffer and group a sum and its base, by group the maximum so far
   float* lbuf = (float*)((uint8_t*)bars + C::BAR_BYTES);     // [OBUF][NG][MT]
   float* mbuf = lbuf + OBUF * NG * MT;                       // [OBUF][NG][MT]
@@ -182,6 +216,10 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       for (int q = 0; q < 4; ++q) mbar_init(&m_full[s * 4 + q], 1);
     }
     for (int s = 0; s < KS; ++s) { mbar_init(&kv_full[s], 1); mbar_init(&kv_empty[s], 1); }
+    for (int s = 0; s < NPIECE; ++s) {
+      mbar_init(&piece_full[s], 1);
+      mbar_init(&piece_empty[s], 3 + (NG + 1) * C::NQ);
+    }
     mbar_init(drain, 1);
     mbar_init(drain + 1, 1);
     *abort_flag = 0;
@@ -204,6 +242,18 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   const uint32_t tmem = *tmem_slot;
   const CacheSplit run = *split;
 
+  // The next piece (a warp calls this): false after the last one, or an abort.
+  uint32_t taken = 0;
+  auto take = [&](Piece& it) -> bool {
+    const int st = taken % NPIECE;
+    if (!warp_wait(&piece_full[st], (taken / NPIECE) & 1, abort_flag, c.status)) return false;
+    it = pieces[st];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&piece_empty[st]);
+    ++taken;
+    return it.u >= 0;
+  };
+
   if (warp < 4) {
   regs_down<kRegsIssue>();
   if (warp == 0) {
@@ -214,13 +264,11 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     const int32_t P = min(1 << c.page_shift, kCacheBox);     // events of a box
     const int np = HT / P;
     const int32_t outside = c.n_pages << c.page_shift;
-    CacheItems<Line> items;
-    items.start(c, run);
-    CacheItem<Line> it;
+    Piece it;
     bool ok = true;
-    while (ok && items.next(c, it)) {
+    while (ok && take(it)) {
       const CacheBlock& blk = it.k;
-      if (it.x.len == 0) continue;
+      if (it.len == 0) continue;
       const int32_t* row = c.table + (int64_t)it.u * c.stride;
       // pool row of this lane's box in half h of the piece's tiles
       auto place = [&](int h) -> int32_t {
@@ -238,7 +286,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         ok = mbar_wait(&q_empty[qb], ((itm / QBUF) & 1) ^ 1, abort_flag, c.status);
         if (ok) {
           mbar_arrive_expect_tx(&q_full[qb], C::Q_BYTES);
-          const int32_t qrow = (int32_t)(it.x.row0 * c.heads + (int64_t)it.b * MT);
+          const int32_t qrow = (int32_t)it.at0;
 #pragma unroll
           for (int s = 0; s < RSUB; ++s)
             tma_load_2d(&tmQ, &q_full[qb], sQ + qb * C::Q_BYTES + s * C::QSUB, s * 64, qrow);
@@ -283,11 +331,9 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     const bool elect = elect_one();
     uint32_t itm = 0, g = 0;               // items, tiles
     bool ok = true;
-    CacheItems<Line> items;
-    items.start(c, run);
-    CacheItem<Line> it;
-    while (ok && items.next(c, it)) {
-      if (it.x.len == 0) continue;
+    Piece it;
+    while (ok && take(it)) {
+      if (it.len == 0) continue;
       const int qb = itm % QBUF;
       if (!warp_wait(&q_full[qb], (itm / QBUF) & 1, abort_flag, c.status)) break;
       const uint64_t ad = sdesc_sw128(smem_u32(sQ + qb * C::Q_BYTES), 16, 1024);
@@ -326,11 +372,9 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     const bool elect = elect_one();
     uint32_t itm = 0, g = 0;               // items, halves
     bool ok = true;
-    CacheItems<Line> items;
-    items.start(c, run);
-    CacheItem<Line> it;
-    while (ok && items.next(c, it)) {
-      if (it.x.len == 0) continue;
+    Piece it;
+    while (ok && take(it)) {
+      if (it.len == 0) continue;
       const int ob = itm % OBUF;
       if (!warp_wait(&o_free[ob], ((itm / OBUF) & 1) ^ 1, abort_flag, c.status)) break;
       for (int i = 2 * it.t0; i < 2 * it.t1; ++i, ++g) {
@@ -359,6 +403,33 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     int dummy = 0;
     mbar_wait(drain + 1, 0, &dummy, c.status);
     __syncwarp();
+  } else {
+    // ------------------------------------------------------------ planner
+    CacheItems<Line> items;
+    items.start(c, run);
+    CacheItem<Line> it;
+    uint32_t n = 0;
+    for (bool more = true; more; ++n) {
+      more = items.next(c, it);
+      const int st = n % NPIECE;
+      if (!warp_wait(&piece_empty[st], ((n / NPIECE) & 1) ^ 1, abort_flag, c.status)) break;
+      if (lane == 0) {
+        Piece q = {};
+        q.u = -1;
+        if (more) {
+          q.u = it.u;
+          q.pair0 = it.b * MT;
+          q.at0 = it.x.row0 * c.heads + q.pair0;
+          q.rows = (int32_t)min((uint32_t)MT, (uint32_t)it.x.n * (uint32_t)c.heads - q.pair0);
+          q.m = it.x.m; q.len = it.x.len;
+          q.t0 = it.t0; q.t1 = it.t1; q.k = it.k;
+          q.parts = it.parts; q.whole = it.whole; q.starts = it.starts;
+        }
+        pieces[st] = q;
+        mbar_arrive(&piece_full[st]);
+      }
+      __syncwarp();
+    }
   }
   } else if (warp < 20) {
   if (quad < C::NQ) {
@@ -373,19 +444,16 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     const float2 mul2 = make_float2(mul, mul);
     uint32_t g = 0, itm = 0;
     bool ok = true;
-    CacheItems<Line> items;
-    items.start(c, run);
-    CacheItem<Line> it;
-    while (ok && items.next(c, it)) {
-      if (it.x.len == 0) continue;
+    Piece it;
+    while (ok && take(it)) {
+      if (it.len == 0) continue;
       const CacheBlock& blk = it.k;
       const int ob = itm % OBUF;
-      const uint32_t pairs = (uint32_t)it.x.n * (uint32_t)c.heads;
-      const uint32_t pair = (uint32_t)it.b * MT + row;
-      const bool valid = pair < pairs;
-      const int32_t pos = valid ? cache_pos(it.x, (int)(pair / (uint32_t)c.heads)) : blk.pmax;
+      const bool valid = row < it.rows;
+      const int j = (int)((uint32_t)(it.pair0 + row) / (uint32_t)c.heads);
+      const int32_t pos = !valid ? blk.pmax : j < it.m ? it.len - it.m + j : it.len - 1;
       const int32_t low = cache_low(c, pos), low_max = cache_low(c, blk.pmax);
-      const bool idle = (uint32_t)it.b * MT + quad * 32 >= pairs;   // no row in this quadrant
+      const bool idle = quad * 32 >= it.rows;          // no row in this quadrant
       float m_run = -INFINITY, l_run = 0.f;     // maximum (log2 units) that the sum is over
       bool poison = false;
       for (int i = 2 * it.t0; i < 2 * it.t1; ++i, ++g) {
@@ -405,12 +473,12 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
           for (int h = 0; h < HT; h += 32) {
             float v[32];
             tmem_ld32(s_addr + h, v);
-            if (masked || p.scale2 <= 0.f) {
-              if (p.scale2 <= 0.f) {
-                const float f = p.scale2 == 0.f ? 0.f : -1.f;
+            if (p.scale2 <= 0.f) {
+              const float f = p.scale2 == 0.f ? 0.f : -1.f;
 #pragma unroll
-                for (int k = 0; k < 32; ++k) v[k] *= f;
-              }
+              for (int k = 0; k < 32; ++k) v[k] *= f;
+            }
+            if (masked) {
               // events that the row sees: [0, hi) without [sk, lo)
               const int32_t t0 = tile0 + h;
               const int hi = max(min(pos + 1 - t0, 32), 0);
@@ -423,25 +491,30 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
               for (int k = 0; k < 32; k += 2)
                 z2 = fma_f2(make_float2(v[k], v[k + 1]), make_float2(0.f, 0.f), z2);
               if (__any_sync(0xffffffffu, valid && !(z2.x + z2.y == 0.f))) {
-                clear = masked;                // a score is not finite
-                if (masked) {
-#pragma unroll
+                // a score is not finite: column by column
+                clear = true;
+#pragma unroll 1
+                for (int k = 0; k < 32; ++k) {
+                  const float x = tmem_ld1(s_addr + h + k);
+                  const bool fin = fabsf(x) < INFINITY;
+                  poison |= valid && !fin && ((vis >> k) & 1);
+                  tmem_st1(s_addr + h + k, fin ? x : -INFINITY);
+                }
+                tmem_ld32(s_addr + h, v);
+                if (p.scale2 <= 0.f) {         // those that were not finite stay -inf
+                  const float f = p.scale2 == 0.f ? 0.f : -1.f;
+#pragma unroll 1
                   for (int k = 0; k < 32; ++k) {
-                    const bool fin = fabsf(v[k]) < INFINITY;
-                    poison |= valid && !fin && ((vis >> k) & 1);
-                    v[k] = fin ? v[k] : -INFINITY;
+                    const float x = tmem_ld1(s_addr + h + k);
+                    tmem_st1(s_addr + h + k, x > -INFINITY ? f * x : x);
                   }
+                  tmem_ld32(s_addr + h, v);
                 }
               }
-              if (masked && sk >= lo) {
 #pragma unroll
-                for (int k = 0; k < 32; ++k) v[k] = k < hi ? v[k] : -INFINITY;
-              } else if (masked) {
-#pragma unroll
-                for (int k = 0; k < 32; ++k) v[k] = (vis >> k) & 1 ? v[k] : -INFINITY;
-              }
-              tmem_st32(s_addr + h, v);
+              for (int k = 0; k < 32; ++k) v[k] = vis & (1u << k) ? v[k] : -INFINITY;
             }
+            if (masked || p.scale2 <= 0.f) tmem_st32(s_addr + h, v);
             float m8[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) m8[k] = fmaxf(fmax3(v[k], v[k + 8], v[k + 16]), v[k + 24]);
@@ -543,18 +616,14 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     const bool writer = warp == 20 && lane == 0;
     if (writer) join->rows = 0;
     uint32_t itm = 0, stg = 0;             // items, staged boxes
-    CacheItems<Line> items;
-    items.start(c, run);
-    CacheItem<Line> it;
-    while (items.next(c, it)) {
-      const uint32_t pairs = (uint32_t)it.x.n * (uint32_t)c.heads;
-      const uint32_t pair = (uint32_t)it.b * MT + row;
-      const bool valid = pair < pairs;
-      const bool box = C::NSTG > 0 && (uint32_t)it.b * MT + quad * 32 + 32 <= pairs;
-      const bool idle = (uint32_t)it.b * MT + quad * 32 >= pairs;
-      const int64_t at = it.x.row0 * c.heads + pair;
+    Piece it;
+    while (take(it)) {
+      const bool valid = row < it.rows;
+      const bool box = C::NSTG > 0 && quad * 32 + 32 <= it.rows;
+      const bool idle = quad * 32 >= it.rows;
+      const int64_t at = it.at0 + row;
       __nv_bfloat16* orow = (__nv_bfloat16*)p.out + at * R;
-      if (it.x.len == 0) {                 // no event: zeros
+      if (it.len == 0) {                 // no event: zeros
         if (!valid) continue;
         for (int k = 0; k < R; k += 16) put32(orow + k, wide, 0, 0, 0, 0, 0, 0, 0, 0);
         if (p.lse) p.lse[at] = -INFINITY;
@@ -650,9 +719,9 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       __syncwarp();
       if (lane == 0) mbar_arrive(&o_free[ob]);
       if (writer && !it.whole && it.starts) {
-        join->pair0 = it.x.row0 * c.heads + (int64_t)it.b * MT;
+        join->pair0 = it.at0;
         join->parts = it.parts;
-        join->rows = (int32_t)min((uint32_t)MT, pairs - (uint32_t)it.b * MT);
+        join->rows = it.rows;
       }
       ++itm;
     }
