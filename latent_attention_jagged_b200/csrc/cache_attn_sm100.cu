@@ -145,20 +145,6 @@ __device__ __forceinline__ void clear_rows(uint8_t* kv, uint32_t sub) {
   fence_proxy_async_smem();
 }
 
-// 32 bytes to dst: one store where it is aligned to them (whole sectors, so rows
-// go straight from the lanes that hold them), two otherwise.
-__device__ __forceinline__ void put32(void* dst, bool wide, uint32_t a, uint32_t b, uint32_t c,
-                                      uint32_t d, uint32_t e, uint32_t f, uint32_t g, uint32_t h) {
-  if (wide) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a),
-                 "r"(b), "r"(c), "r"(d), "r"(e), "r"(f), "r"(g), "r"(h)
-                 : "memory");
-  } else {
-    ((uint4*)dst)[0] = make_uint4(a, b, c, d);
-    ((uint4*)dst)[1] = make_uint4(e, f, g, h);
-  }
-}
-
 template <int R, int MT>
 __global__ void __launch_bounds__(kThreads, 1)
 cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmC,
@@ -611,7 +597,6 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     // ------------------------------------------------------------ epilogue
     const int row = quad * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
-    const bool wide = ((uintptr_t)p.out & 31) == 0;
     CacheJoin* join = p.join + blockIdx.x;
     const bool writer = warp == 20 && lane == 0;
     if (writer) join->rows = 0;
@@ -625,7 +610,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       __nv_bfloat16* orow = (__nv_bfloat16*)p.out + at * R;
       if (it.len == 0) {                 // no event: zeros
         if (!valid) continue;
-        for (int k = 0; k < R; k += 16) put32(orow + k, wide, 0, 0, 0, 0, 0, 0, 0, 0);
+        for (int k = 0; k < R; k += 8) *(uint4*)(orow + k) = make_uint4(0, 0, 0, 0);
         if (p.lse) p.lse[at] = -INFINITY;
         if (p.lse2) p.lse2[at] = -INFINITY;
         continue;
@@ -683,12 +668,14 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
           for (int k = box ? R : 0; k < R; k += 32) {
             float v[32];
             tmem_ld32(o_addr + k, v);
-            uint32_t x[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) x[j] = pack_bf16(v[2 * j] * inv, v[2 * j + 1] * inv);
             if (valid) {
-              put32(orow + k, wide, x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]);
-              put32(orow + k + 16, wide, x[8], x[9], x[10], x[11], x[12], x[13], x[14], x[15]);
+#pragma unroll
+              for (int j = 0; j < 32; j += 8)
+                *(uint4*)(orow + k + j) =
+                    make_uint4(pack_bf16(v[j] * inv, v[j + 1] * inv),
+                               pack_bf16(v[j + 2] * inv, v[j + 3] * inv),
+                               pack_bf16(v[j + 4] * inv, v[j + 5] * inv),
+                               pack_bf16(v[j + 6] * inv, v[j + 7] * inv));
             }
           }
           if (valid) {
@@ -704,12 +691,10 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
           for (int k = 0; k < R; k += 32) {
             float v[32];
             tmem_ld32(o_addr + k, v);
-            const uint32_t* x = (const uint32_t*)v;
             if (valid) {
 #pragma unroll
-              for (int j = 0; j < 32; j += 8)
-                put32(prow + k + j, true, x[j], x[j + 1], x[j + 2], x[j + 3], x[j + 4], x[j + 5],
-                      x[j + 6], x[j + 7]);
+              for (int j = 0; j < 32; j += 4)
+                *(float4*)(prow + k + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
             }
           }
           if (valid) p.part_ml[slot] = make_float2(m, l);

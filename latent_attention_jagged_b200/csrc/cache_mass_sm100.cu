@@ -30,20 +30,25 @@ using namespace tc;
 
 namespace {
 
-constexpr int KT = 128;
+constexpr int KT = 128;                   // events of a tile
+constexpr int NP = 128;                   // pairs of a block
 
-template <int R, int NP>
+// Two groups of 8 warps take the blocks of pairs in turn; of a group, two warps share
+// 32 events (half of the pairs each).
+constexpr int kSoft0 = 2, kSoft = 16;
+constexpr int kThreads = 32 * (kSoft0 + kSoft);
+
+template <int R>
 struct Cfg {
   static constexpr int RSUB = R / 64;
   static constexpr int CP = NP / 2;                    // pairs of a softmax warp
   static constexpr int SB = 4;                         // S^T buffers in tensor memory
-  // ring slots: single tokens reread the events, long chunks the queries
-  static constexpr int KS = NP == 32 ? (R == 256 ? 3 : 6) : (R == 256 ? 1 : 2);
-  static constexpr int QS = NP == 32 ? (R == 256 ? 2 : 4) : (R == 256 ? 2 : 4);
+  static constexpr int KS = R == 256 ? 1 : 2;          // ring slots: a tile stays for many blocks
+  static constexpr int QS = R == 256 ? 2 : 4;
   static constexpr uint32_t KSUB = KT * 128, K_BYTES = RSUB * KSUB;
   static constexpr uint32_t QSUB = NP * 128, Q_BYTES = RSUB * QSUB;
   static constexpr uint32_t BAR_BYTES = R == 256 ? 256 : 384;
-  static constexpr uint32_t F_BYTES = 8 * CP * 8 + 128 * 4;   // log sums, positions; sums
+  static constexpr uint32_t F_BYTES = kSoft * CP * 12 + 3 * 128 * 4;   // of the pairs; sums
   static constexpr size_t SMEM = 1024 + KS * K_BYTES + QS * Q_BYTES + BAR_BYTES + F_BYTES;
   static constexpr uint32_t TMEM_COLS = SB * NP;
   static_assert(SMEM <= 232448, "shared memory budget");
@@ -52,34 +57,12 @@ struct Cfg {
   static_assert(KS * K_BYTES + QS * Q_BYTES <= 229376, "rings");
 };
 
-constexpr int kSoft0 = 2, kSoft = 8;
-constexpr int kThreads = 32 * (kSoft0 + kSoft);
 
-template <int CP>
-__device__ __forceinline__ void tmem_ld_cp(uint32_t taddr, float (&v)[CP]) {
-  if constexpr (CP == 64) {
-    tmem_ld64(taddr, v);
-  } else {
-    static_assert(CP == 16, "column counts");
-    uint32_t r[16];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-  }
-}
-
-template <int R, int NP>
+template <int R>
 __global__ void __launch_bounds__(kThreads, 1)
 cache_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmC,
                   const CacheAttn p) {
-  using C = Cfg<R, NP>;
+  using C = Cfg<R>;
   using Line = ByTiles<NP, KT>;
   constexpr int CP = C::CP, RSUB = C::RSUB, KS = C::KS, QS = C::QS, SB = C::SB;
   extern __shared__ uint8_t smem_raw[];
@@ -93,16 +76,15 @@ cache_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   uint64_t* q_empty = q_full + QS;         // [QS]
   uint64_t* s_full = q_empty + QS;         // [SB]
   uint64_t* s_empty = s_full + SB;         // [SB] every softmax warp has read S^T
-  uint64_t* pair_bar = s_empty + SB;       // [4] the two softmax warps of a lane quadrant
+  uint64_t* pair_bar = s_empty + SB;       // [4] the four softmax warps of a lane quadrant
   uint64_t* drain = pair_bar + 4;
   uint32_t* tmem_slot = (uint32_t*)(drain + 1);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   CacheSplit* split = (CacheSplit*)(tmem_slot + 2);
   static_assert((2 * KS + 2 * QS + 2 * SB + 5) * 8 + 8 + sizeof(CacheSplit) <= C::BAR_BYTES,
                 "barriers");
-  float* sums = (float*)((uint8_t*)bars + C::BAR_BYTES);   // [128]
-  float* lbuf = sums + 128;                                  // [8 warps][CP] log sums
-  int32_t* pbuf = (int32_t*)(lbuf + 8 * CP);                 // [8 warps][CP] positions
+  float* sums = (float*)((uint8_t*)bars + C::BAR_BYTES);   // [3][128]
+  float* pbuf = sums + 3 * 128;                              // [kSoft][3][CP] of the pairs
 
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -111,8 +93,8 @@ cache_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   if (threadIdx.x == 0) {
     for (int s = 0; s < KS; ++s) { mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 1); }
     for (int s = 0; s < QS; ++s) { mbar_init(&q_full[s], 1); mbar_init(&q_empty[s], 1); }
-    for (int s = 0; s < SB; ++s) { mbar_init(&s_full[s], 1); mbar_init(&s_empty[s], kSoft); }
-    for (int q = 0; q < 4; ++q) mbar_init(&pair_bar[q], 2);
+    for (int s = 0; s < SB; ++s) { mbar_init(&s_full[s], 1); mbar_init(&s_empty[s], kSoft / 2); }
+    for (int q = 0; q < 4; ++q) mbar_init(&pair_bar[q], 4);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -232,10 +214,13 @@ cache_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax
-    const int quad = warp & 3, part = (warp - kSoft0) >> 2;   // event quadrant, half of the pairs
+    const int quad = warp & 3, part = ((warp - kSoft0) >> 2) & 1;   // events, half of the pairs
+    const int group = (warp - kSoft0) >> 3;
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
-    float* lw = lbuf + (warp - kSoft0) * CP;
-    int32_t* pw = pbuf + (warp - kSoft0) * CP;
+    // of this warp's pairs: log sum, last and first event inside the window
+    float* lw = pbuf + (warp - kSoft0) * 3 * CP;
+    int32_t* pw = (int32_t*)(lw + CP);
+    int32_t* ww = pw + CP;
     CacheJoin* join = p.join + blockIdx.x;
     const bool writer = warp == kSoft0 && lane == 0;
     if (writer) join->rows = 0;
@@ -249,62 +234,61 @@ cache_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       const int32_t tile0 = it.k.tile * KT;
       const int32_t t = tile0 + quad * 32 + lane;          // this lane's event
       const uint32_t pairs = (uint32_t)it.x.n * (uint32_t)c.heads;
+      // the first events are inside every window
+      const int32_t tw = t < c.n_sink ? INT32_MAX : t;
       float sum = 0.f;
       for (int i = it.t0; i < it.t1; ++i, ++qn) {
+        if ((int)(qn & 1) != group) continue;
         const int sb = qn % SB;
-        // this warp's pairs: log sums and positions, one or two a lane
         const uint32_t pair0 = (uint32_t)(it.k.first + i) * NP + part * CP;
         __syncwarp();
 #pragma unroll
         for (int k = lane; k < CP; k += 32) {
           const uint32_t pair = pair0 + k;
           const bool in = pair < pairs;
+          const int32_t pos = in ? cache_pos(it.x, (int)(pair / (uint32_t)c.heads)) : -1;
           lw[k] = in ? p.lse2[it.x.row0 * c.heads + pair] : 0.f;
-          pw[k] = in ? cache_pos(it.x, (int)(pair / (uint32_t)c.heads)) : -1;
+          pw[k] = pos;
+          ww[k] = cache_low(c, pos);
         }
         __syncwarp();
         bool w = mbar_wait(&s_full[sb], (qn / SB) & 1, abort_flag, c.status);
         if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
         tc_fence_after();
-        float v[CP];
-        tmem_ld_cp<CP>(lane_base + sb * NP + part * CP, v);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_empty[sb]);
-        if (pair0 >= pairs) continue;
         float s4[4] = {0.f, 0.f, 0.f, 0.f};
-        // every pair here sees every event of the quadrant?
-        const int32_t first = pw[0], last = pw[CP - 1];
-        const bool full = last >= tile0 + quad * 32 + 31 && pair0 + CP <= pairs &&
-                          (c.window == 0 || cache_low(c, last) <= tile0 + quad * 32) &&
-                          first >= tile0 + quad * 32 + 31;
-        if (full) {
-#pragma unroll
-          for (int k = 0; k < CP; k += 4) {
-            const float4 l4 = *(const float4*)(lw + k);
-            s4[0] += ex2_approx(fmaf(v[k], p.scale2, -l4.x));
-            s4[1] += ex2_approx(fmaf(v[k + 1], p.scale2, -l4.y));
-            s4[2] += ex2_approx(fmaf(v[k + 2], p.scale2, -l4.z));
-            s4[3] += ex2_approx(fmaf(v[k + 3], p.scale2, -l4.w));
+#pragma unroll 1
+        for (int h = 0; h < CP; h += 32) {
+          float v[32];
+          tmem_ld32(lane_base + sb * NP + part * CP + h, v);
+          if (h + 32 == CP) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_empty[sb]);
           }
-        } else {
-          const bool sink = t < c.n_sink || c.window == 0;
 #pragma unroll
-          for (int k = 0; k < CP; ++k) {
-            const int32_t pos = pw[k];
-            const bool see = t <= pos && (sink || t > pos - c.window);
-            const float e = ex2_approx(fmaf(v[k], p.scale2, -lw[k]));
-            s4[k & 3] += see ? e : 0.f;
+          for (int k = 0; k < 32; k += 4) {
+            const float4 l4 = *(const float4*)(lw + h + k);
+            const int4 p4 = *(const int4*)(pw + h + k), w4 = *(const int4*)(ww + h + k);
+            const float e0 = ex2_approx(fmaf(v[k], p.scale2, -l4.x));
+            const float e1 = ex2_approx(fmaf(v[k + 1], p.scale2, -l4.y));
+            const float e2 = ex2_approx(fmaf(v[k + 2], p.scale2, -l4.z));
+            const float e3 = ex2_approx(fmaf(v[k + 3], p.scale2, -l4.w));
+            if (t <= p4.x && tw >= w4.x) s4[0] += e0;
+            if (t <= p4.y && tw >= w4.y) s4[1] += e1;
+            if (t <= p4.z && tw >= w4.z) s4[2] += e2;
+            if (t <= p4.w && tw >= w4.w) s4[3] += e3;
           }
         }
         sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
       }
       if (!ok) break;
-      // the two halves of the pairs meet
-      if (part == 1) sums[quad * 32 + lane] = sum;
+      // the groups' halves of the pairs meet, in this order
+      const int lead = group * 2 + part;
+      if (lead) sums[(lead - 1) * 128 + quad * 32 + lane] = sum;
       if (!group_sync(&pair_bar[quad], pphase, abort_flag, c.status)) break;
-      if (part == 0) {
-        sum += sums[quad * 32 + lane];
+      if (lead == 0) {
+#pragma unroll
+        for (int k = 0; k < 3; ++k) sum += sums[k * 128 + quad * 32 + lane];
         if (!it.whole) {
           p.part_ml[((int64_t)blockIdx.x * 2 + (it.starts ? 1 : 0)) * KT + quad * 32 + lane].x = sum;
         } else if (t <= all.pmax && (t >= cache_low(c, all.pmin) || t < c.n_sink)) {
@@ -346,14 +330,14 @@ __global__ void __launch_bounds__(KT) cache_mass_join_kernel(const CacheAttn p) 
   if (at >= 0) atomicAdd(&p.mass[at], sum);
 }
 
-template <int R, int NP>
+template <int R>
 cudaError_t launch_rn(const CacheAttn& a, const CUtensorMap& tmC, int num_sms, cudaStream_t s) {
-  using C = Cfg<R, NP>;
+  using C = Cfg<R>;
   static uint64_t attr_devices = 0;
   int dev = 0;
   cudaGetDevice(&dev);
   if (!(attr_devices >> (dev & 63) & 1)) {
-    cudaError_t e = cudaFuncSetAttribute(cache_mass_kernel<R, NP>,
+    cudaError_t e = cudaFuncSetAttribute(cache_mass_kernel<R>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
     if (e != cudaSuccess) return e;
     attr_devices |= 1ull << (dev & 63);
@@ -361,7 +345,7 @@ cudaError_t launch_rn(const CacheAttn& a, const CUtensorMap& tmC, int num_sms, c
   CUtensorMap tmQ;
   if (!make_tmap_bf16(&tmQ, a.q, (uint64_t)a.c.rows * a.c.heads, R, NP))
     return cudaErrorInvalidValue;
-  cudaError_t e = launch_dependent(cache_mass_kernel<R, NP>, dim3(num_sms), dim3(kThreads),
+  cudaError_t e = launch_dependent(cache_mass_kernel<R>, dim3(num_sms), dim3(kThreads),
                                    C::SMEM, s, 1, tmQ, tmC, a);
   if (e != cudaSuccess) return e;
   return launch_dependent(cache_mass_join_kernel, dim3(num_sms), dim3(KT), 0, s, 1, a);
@@ -371,7 +355,7 @@ template <int R>
 cudaError_t launch_r(const CacheAttn& a, const CUtensorMap& tmC, int num_sms, cudaStream_t s) {
   if (a.pairs <= 16 * (int64_t)a.c.B)
     return launch_cache_mass_token(a, tmC, num_sms, s);
-  return launch_rn<R, 128>(a, tmC, num_sms, s);
+  return launch_rn<R>(a, tmC, num_sms, s);
 }
 
 }  // namespace

@@ -127,6 +127,7 @@ struct CacheSplit {
 struct CacheSplitSpace {
   int32_t prefix[LLATTE_CACHE_MAX_BATCH + 4];
   int2 user[LLATTE_CACHE_MAX_BATCH];        // rows, cached events
+  int64_t row0[LLATTE_CACHE_MAX_BATCH];     // first row
 };
 
 // The cut at place `at` of `base` (a whole warp calls this): where it lies and the
@@ -154,7 +155,7 @@ __device__ __forceinline__ void cache_cut(const CacheCall& c, const CacheSplitSp
   }
   s->u = lo;
   const int2 d = w.user[lo];
-  const CacheUser x = {0, d.x, max(0, d.x - c.n_cand), d.y};
+  const CacheUser x = {w.row0[lo], d.x, max(0, d.x - c.n_cand), d.y};
   s->x = x;
   const int nb = W::blocks(c, x);
   int32_t left = (int32_t)at - w.prefix[lo];
@@ -207,6 +208,7 @@ __device__ __forceinline__ void cache_split(const CacheCall& c, int min_quota, b
       places = -1;
     }
     w.user[u] = make_int2(x.n, x.len);
+    w.row0[u] = x.row0;
     w.prefix[u + 1] = (int32_t)min(places, kTop - 1);
   }
   // users of many blocks: a warp each, a block per lane
@@ -304,7 +306,6 @@ struct CacheItems {
     nb = 0;
     if (pos < end) {
       x = s.x;
-      x.row0 = c.qoff[u];
       nb = W::blocks(c, x);
       fetch(c, u + 1);
     }
