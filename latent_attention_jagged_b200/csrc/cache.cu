@@ -557,6 +557,12 @@ CacheCall make_call(const llatte_cache* h, const llatte_cache_view* v, const int
   c.cap = (int64_t)std::min(v->table_stride, h->dims.max_pages) * h->dims.page_size;
   c.n_pages = h->dims.n_pages; c.page_shift = h->page_shift;
   c.heads = h->dims.heads; c.r = h->dims.rank; c.status = h->status;
+  if (c.heads > 1) {         // see cache_div
+    int sh = 0;
+    while (((int64_t)1 << sh) < c.heads) ++sh;
+    c.head_mul = (uint32_t)((((uint64_t)1 << (31 + sh)) / (uint64_t)c.heads) + 1);
+    c.head_shift = sh - 1;
+  }
   return c;
 }
 

@@ -20,6 +20,8 @@ struct CacheCall {
   int32_t stride, B;
   int32_t n_pages, page_shift;   // page size = 1 << page_shift
   int32_t heads, r;
+  uint32_t head_mul;         // division by heads (cache_div); 0 for one head
+  int32_t head_shift;
   int32_t n_cand, window, n_sink;
   int32_t* status;
 };

@@ -436,7 +436,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       const CacheBlock& blk = it.k;
       const int ob = itm % OBUF;
       const bool valid = row < it.rows;
-      const int j = (int)((uint32_t)(it.pair0 + row) / (uint32_t)c.heads);
+      const int j = cache_div(c, it.pair0 + row);
       const int32_t pos = !valid ? blk.pmax : j < it.m ? it.len - it.m + j : it.len - 1;
       const int32_t low = cache_low(c, pos), low_max = cache_low(c, blk.pmax);
       const bool idle = quad * 32 >= it.rows;          // no row in this quadrant

@@ -14,6 +14,13 @@ struct CacheUser {
   int32_t len;       // cached events
 };
 
+// n / heads for 0 <= n < 2^31.  With 2^(s-1) < heads <= 2^s and m = floor(2^(31+s) /
+// heads) + 1 < 2^32, m heads = 2^(31+s) + e with 0 < e <= 2^s, so that n m / 2^(31+s)
+// exceeds n / heads by n e / (heads 2^(31+s)) < 1 / heads: the quotient is exact.
+__device__ __forceinline__ int32_t cache_div(const CacheCall& c, uint32_t n) {
+  return (int32_t)(c.head_mul ? __umulhi(n, c.head_mul) >> c.head_shift : n);
+}
+
 // A user of the call from its offsets and length; a user the header leaves out
 // (bad offsets or length) gets no rows and no events, and its fault goes to the
 // status word.

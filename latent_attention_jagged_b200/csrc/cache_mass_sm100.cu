@@ -246,7 +246,7 @@ cache_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         for (int k = lane; k < CP; k += 32) {
           const uint32_t pair = pair0 + k;
           const bool in = pair < pairs;
-          const int32_t pos = in ? cache_pos(it.x, (int)(pair / (uint32_t)c.heads)) : -1;
+          const int32_t pos = in ? cache_pos(it.x, cache_div(c, pair)) : -1;
           lw[k] = in ? p.lse2[it.x.row0 * c.heads + pair] : 0.f;
           pw[k] = pos;
           ww[k] = cache_low(c, pos);

@@ -36,8 +36,8 @@ __device__ __forceinline__ CacheBlock cache_block(const CacheCall& c, const Cach
   // pairs of a call fit 31 bits, so 32-bit unsigned arithmetic is exact
   const uint32_t pairs = (uint32_t)x.n * (uint32_t)c.heads;
   const uint32_t q0 = (uint32_t)b * MT, q1 = min(q0 + MT, pairs) - 1;
-  k.pmin = cache_pos(x, (int)(q0 / (uint32_t)c.heads));
-  k.pmax = cache_pos(x, (int)(q1 / (uint32_t)c.heads));
+  k.pmin = cache_pos(x, cache_div(c, q0));
+  k.pmax = cache_pos(x, cache_div(c, q1));
   const int32_t all = k.pmax < 0 ? 0 : k.pmax / KT + 1;
   k.first_tile = cache_low(c, k.pmin) / KT;
   const int32_t sink = min(c.n_sink, k.pmax + 1);

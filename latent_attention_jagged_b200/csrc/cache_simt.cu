@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(256) cache_rows_kernel(CacheAttn p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int row = min(4 * ty + i, rows - 1);
-      pos[i] = cache_pos(it.x, (int)((pair0 + row) / (uint32_t)c.heads));
+      pos[i] = cache_pos(it.x, cache_div(c, pair0 + row));
       low[i] = cache_low(c, pos[i]);
       m[i] = -INFINITY;
       l[i] = 0.f;
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(256) cache_tokens_kernel(CacheAttn p) {
         if (a >= rows) break;
         s[a] = (s2[a].x + s2[a].y) * p.scale2;
         if (masked) {
-          const int32_t pos = cache_pos(it.x, (int)((pair0 + a) / (uint32_t)c.heads));
+          const int32_t pos = cache_pos(it.x, cache_div(c, pair0 + a));
           const bool fin = fabsf(s[a]) < INFINITY;
           const bool see = t <= pos && (t >= cache_low(c, pos) || t < c.n_sink);
           odd |= !fin;
@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(256) cache_mass_rows_kernel(CacheAttn p) {
       copy_commit();
       if (tid < MT) {
         s_lse[tid] = tid < rows ? p.lse2[at0 + tid] : 0.f;
-        s_pos[tid] = tid < rows ? cache_pos(it.x, (int)((pair0 + tid) / (uint32_t)c.heads)) : -1;
+        s_pos[tid] = tid < rows ? cache_pos(it.x, cache_div(c, pair0 + tid)) : -1;
       }
       copy_wait<0>();
       __syncthreads();

@@ -226,7 +226,7 @@ cache_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn p) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int32_t r = min(grp + 8 * h, rows - 1);
-        pos[h] = cache_pos(it.x, (int)((uint32_t)(pair0 + r) / (uint32_t)c.heads));
+        pos[h] = cache_pos(it.x, cache_div(c, (uint32_t)(pair0 + r)));
         low[h] = cache_low(c, pos[h]);
       }
       const int32_t low_max = cache_low(c, it.k.pmax);
@@ -526,7 +526,7 @@ cache_mass_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn
             for (int e = 0; e < 2; ++e) {
               const int a = 8 * n + 2 * t4 + e;        // this lane's column
               lse[n][e] = a < rows ? p.lse2[at0 + a] : 0.f;
-              pos[n][e] = a < rows ? cache_pos(it.x, (b * MT + a) / c.heads) : -1;
+              pos[n][e] = a < rows ? cache_pos(it.x, cache_div(c, b * MT + a)) : -1;
             }
         }
         float s[2][4];
