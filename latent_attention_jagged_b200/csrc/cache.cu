@@ -30,6 +30,7 @@ struct llatte_cache {
   float* part_o;         // [2 num_sms, block rows, rank]
   float2* part_ml;       // [2 num_sms, block rows]
   CacheJoin* join;       // [num_sms]
+  int32_t* parts;        // [num_sms]
 };
 
 namespace llatte {
@@ -508,7 +509,7 @@ bool cache_uses_tc(const llatte_cache_dims& d) {
   return d.dtype == LLATTE_BF16 && cache_attn_tc_supported(d.rank);
 }
 
-struct CacheLayout { size_t status, count, list, lse2, part_o, part_ml, join, total; };
+struct CacheLayout { size_t status, count, list, lse2, part_o, part_ml, join, parts, total; };
 
 // The parts' slots are counted for the largest part there is (148 SMs); a device
 // with more SMs runs as many CTAs as there are slots.
@@ -526,6 +527,7 @@ CacheLayout cache_layout(const llatte_cache_dims& d) {
   L.part_o = take(sizeof(float) * slots * d.rank);
   L.part_ml = take(sizeof(float2) * slots);
   L.join = take(sizeof(CacheJoin) * kCacheCtas);
+  L.parts = take(sizeof(int32_t) * kCacheCtas);
   L.total = o;
   return L;
 }
@@ -572,6 +574,7 @@ CacheAttn make_attn(const llatte_cache* h, const llatte_cache_view* v, const voi
   a.c = make_call(h, v, qoff, rows);
   a.pool = h->pool; a.mass = h->mass; a.q = q; a.out = out;
   a.part_o = h->part_o; a.part_ml = h->part_ml; a.join = h->join;
+  a.count = h->parts;
   return a;
 }
 
@@ -671,6 +674,7 @@ int llatte_cache_create(llatte_cache** out, const llatte_cache_dims* dims, void*
   h->part_o = (float*)(h->ws + L.part_o);
   h->part_ml = (float2*)(h->ws + L.part_ml);
   h->join = (CacheJoin*)(h->ws + L.join);
+  h->parts = (int32_t*)(h->ws + L.parts);
   if (h->tc) {
     const uint64_t rows = (uint64_t)dims->n_pages * dims->page_size;
     if (!make_tmap_bf16(&h->tmC, pool, rows, dims->rank, std::min(dims->page_size, kCacheBox))) {

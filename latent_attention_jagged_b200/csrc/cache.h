@@ -45,6 +45,7 @@ struct CacheAttn {
   float* part_o;             // [2 CTAs, block rows, r] unnormalised sums
   float2* part_ml;           // [2 CTAs, block rows] maximum (log2 units) and sum
   CacheJoin* join;           // [CTAs]
+  int32_t* count;            // [CTAs] parts done of the block that begins there; 0 between calls
   int64_t pairs;             // (row, head) pairs of the call, as far as the host can tell
   int32_t min_quota;         // fewest tiles of a CTA's run
   bool never_cut;            // no block is cut between CTAs (then there is nothing to join)

@@ -279,7 +279,8 @@ struct CacheItem {
   int32_t t0, t1;
   bool whole;                  // the block is not cut
   bool starts;                 // it starts in this CTA
-  int32_t parts;               // CTAs that share it
+  int32_t parts;               // CTAs that share it, from CTA `lead` on
+  int32_t lead;
 };
 
 // Walks the pieces of this CTA's run.  The next user's offsets and length are
@@ -327,7 +328,8 @@ struct CacheItems {
     it.t1 = min(places, t + (end - pos));
     const int32_t g0 = pos - t;             // the block's first place in the line
     it.whole = it.t0 == 0 && it.t1 == places;
-    it.parts = (g0 + places - 1) / quota - g0 / quota + 1;
+    it.lead = g0 / quota;
+    it.parts = (g0 + places - 1) / quota - it.lead + 1;
     it.starts = it.t0 == 0;
     pos += it.t1 - it.t0;
     t = 0;

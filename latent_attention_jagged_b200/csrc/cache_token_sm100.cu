@@ -18,6 +18,7 @@
 
 #include "cache.h"
 #include "cache_call.cuh"
+#include "cache_issue.cuh"
 #include "cache_sched.cuh"
 #include "tc_common.cuh"
 #include "tc_drain.cuh"
@@ -114,6 +115,7 @@ cache_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn p) {
   uint64_t* kv_full = bars;                // [KS]
   uint64_t* kv_empty = kv_full + KS;       // [KS]
   volatile int* abort_flag = (volatile int*)(kv_empty + KS);
+  volatile int* last_flag = abort_flag + 1;
   CacheSplit* split = (CacheSplit*)(kv_empty + KS + 1);
   static_assert((2 * KS + 2) * 8 + sizeof(CacheSplit) <= C::BAR_BYTES, "barriers");
   float* sm_m = (float*)((uint8_t*)bars + C::BAR_BYTES);   // [NW][MT]
@@ -143,6 +145,7 @@ cache_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn p) {
     // ------------------------------------------------------------ producer
     // Lane l < boxes of a tile gathers box l (as in cache_attn_sm100.cu).
     uint32_t g = 0;
+    const uint64_t policy = policy_stream(!p.lse2);   // the accumulation reads them again
     const int32_t P = min(1 << c.page_shift, kCacheBox);
     const int np = KT / P;
     const int32_t outside = c.n_pages << c.page_shift;
@@ -173,7 +176,7 @@ cache_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn p) {
           uint8_t* dst = sKV + st * C::KV_BYTES + lane * P * 128;
 #pragma unroll
           for (int s = 0; s < RSUB; ++s)
-            tma_load_2d(&tmC, &kv_full[st], dst + s * C::KV_SUB, s * 64, y);
+            tma_load_2d_hint(&tmC, &kv_full[st], dst + s * C::KV_SUB, s * 64, y, policy);
         }
         y = y_next;
       }
@@ -189,8 +192,6 @@ cache_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn p) {
     CacheItem<Line> it;
     // ------------------------------------------------------------ consumers
     const int grp = lane >> 2, t4 = lane & 3;          // row (and row + 8), column pair
-    CacheJoin* join = p.join + blockIdx.x;
-    if (threadIdx.x == 0) join->rows = 0;
     uint32_t g = 0;
     bool ok = true;
     // ldmatrix rows of this lane: events 8 * (lane / 16) + lane % 8 for S, and
@@ -352,8 +353,12 @@ cache_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn p) {
         for (int k = 0; k < NW; ++k) mall = fmaxf(mall, sm_m[k * MT + grp + 8 * h]);
         f[h] = m[h] > -INFINITY ? ex2_approx(m[h] - mall) : 0.f;
       }
-      // sums 4 columns of a row; the rows past 8 only where there are any
-      const int halves = rows > 8 ? 2 : 1, row = threadIdx.x >> 4, c4 = threadIdx.x & 15;
+      // A round sums 128 results of 16 (row, 64 columns): of 16 rows, or, where there
+      // are no more than 8, of 8 rows and twice the columns.  A thread sums 4 columns
+      // of a row.  Column pairs are XORed with the row, so that the 8 rows of a store
+      // fall on different banks.
+      const bool few = rows <= 8;
+      const int line = threadIdx.x >> 4, c4 = threadIdx.x & 15, row = few ? line & 7 : line;
       float mall = -INFINITY, lall = 0.f;
 #pragma unroll
       for (int k = 0; k < NW; ++k) mall = fmaxf(mall, sm_m[k * MT + row]);
@@ -364,27 +369,20 @@ cache_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn p) {
       if (mall == INFINITY) lall = NAN;
       const int64_t slot = ((int64_t)blockIdx.x * 2 + (it.starts ? 1 : 0)) * MT + row;
       const float inv = lall != 0.f ? 1.f / lall : 0.f;
+      auto put = [&](int unit, int q, int h) {
 #pragma unroll
-      for (int q = 0; q < R / 64; ++q) {
-        // column pairs XORed with the row, so that the 8 rows of a store fall on
-        // different banks
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (h >= halves) continue;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int r = grp + 8 * h;
-            ((float2*)meet)[(warp * MT + r) * 32 + ((4 * k + t4) ^ ((r & 7) << 2))] =
-                make_float2(o[8 * q + k][2 * h] * f[h], o[8 * q + k][2 * h + 1] * f[h]);
-          }
-        }
+        for (int k = 0; k < 8; ++k)
+          ((float2*)meet)[(warp * MT + 8 * unit + grp) * 32 + ((4 * k + t4) ^ (grp << 2))] =
+              make_float2(o[8 * q + k][2 * h] * f[h], o[8 * q + k][2 * h + 1] * f[h]);
+      };
+      auto gather = [&](int q) {             // columns 64 q ..
         meet_sync();
-        if (row < rows) {
+        if (row < rows && q < R / 64) {
           float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int k = 0; k < NW; ++k) {
             const float4 y = *(const float4*)(
-                meet + ((k * MT + row) * 32 + ((2 * c4) ^ ((row & 7) << 2))) * 2);
+                meet + ((k * MT + line) * 32 + ((2 * c4) ^ ((line & 7) << 2))) * 2);
             x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
           }
           if (it.whole)
@@ -394,8 +392,23 @@ cache_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn p) {
             *(float4*)(p.part_o + slot * R + q * 64 + c4 * 4) = x;
         }
         meet_sync();
+      };
+      if (few) {
+#pragma unroll
+        for (int q = 0; q < R / 64; q += 2) {
+          put(0, q, 0);
+          if (q + 1 < R / 64) put(1, q + 1, 0);
+          gather(q + (line >> 3));
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < R / 64; ++q) {
+          put(0, q, 0);
+          put(1, q, 1);
+          gather(q);
+        }
       }
-      if (c4 == 0 && row < rows) {
+      if (c4 == 0 && row < rows && !(few && line >= 8)) {
         if (it.whole) {
           const float l2 = lall != 0.f ? mall + log2f(lall) : -INFINITY;
           if (p.lse) p.lse[at0 + row] = l2 * kLn2;
@@ -404,10 +417,53 @@ cache_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn p) {
           p.part_ml[slot] = make_float2(mall, lall);
         }
       }
-      if (threadIdx.x == 0 && !it.whole && it.starts) {
-        join->pair0 = at0;
-        join->parts = it.parts;
-        join->rows = rows;
+      if (it.whole) continue;
+      // ---- a cut block: the CTA that comes last joins the parts, in the order of the
+      // events (all CTAs come: none leaves its run early)
+      __threadfence();
+      meet_sync();
+      if (threadIdx.x == 0) *last_flag = atomicAdd(&p.count[it.lead], 1) == it.parts - 1;
+      meet_sync();
+      if (!*last_flag) continue;
+      __threadfence();
+      if (threadIdx.x == 0) p.count[it.lead] = 0;        // for the next call
+      for (int r = warp; r < rows; r += NW) {
+        auto at_part = [&](int i) -> int64_t {
+          return ((int64_t)(it.lead + i) * 2 + (i == 0 ? 1 : 0)) * MT + r;
+        };
+        float mj = -INFINITY, lj = 0.f;
+        for (int i = lane; i < it.parts; i += 32) mj = fmaxf(mj, __ldcg(&p.part_ml[at_part(i)].x));
+        mj = warp_max(mj);
+        const float mju = mj > -INFINITY ? mj : 0.f;
+        for (int i = lane; i < it.parts; i += 32) {
+          const float2 ml = __ldcg(&p.part_ml[at_part(i)]);
+          lj = fmaf(ex2_approx(ml.x - mju), ml.y, lj);
+        }
+        lj = warp_sum(lj);
+        constexpr int CV = R / 64;           // column pairs of a lane
+        float2 x[CV];
+#pragma unroll
+        for (int k = 0; k < CV; ++k) x[k] = make_float2(0.f, 0.f);
+#pragma unroll 2
+        for (int i = 0; i < it.parts; ++i) {
+          const float w = ex2_approx(__ldcg(&p.part_ml[at_part(i)].x) - mju);
+          const float2* src = (const float2*)(p.part_o + at_part(i) * R);
+#pragma unroll
+          for (int k = 0; k < CV; ++k) {
+            const float2 y = __ldcg(src + lane + 32 * k);
+            x[k].x = fmaf(w, y.x, x[k].x);
+            x[k].y = fmaf(w, y.y, x[k].y);
+          }
+        }
+        const float invj = lj != 0.f ? 1.f / lj : 0.f;
+        uint32_t* dst = (uint32_t*)((__nv_bfloat16*)p.out + (at0 + r) * R);
+#pragma unroll
+        for (int k = 0; k < CV; ++k) dst[lane + 32 * k] = pack_bf16(x[k].x * invj, x[k].y * invj);
+        if (lane == 0) {
+          const float l2 = lj != 0.f ? mj + log2f(lj) : -INFINITY;
+          if (p.lse) p.lse[at0 + r] = l2 * kLn2;
+          if (p.lse2) p.lse2[at0 + r] = l2;
+        }
       }
     }
   }
@@ -599,10 +655,8 @@ cudaError_t launch_r(CacheAttn a, const CUtensorMap& tmC, int num_sms, cudaStrea
     if (f.numRegs * 3 < 2 * kRegsConsume + kRegsProduce) return cudaErrorInvalidConfiguration;
     attr_devices |= 1ull << (dev & 63);
   }
-  cudaError_t e = launch_dependent(cache_token_kernel<R>, dim3(num_sms), dim3(kThreads), C::SMEM, s,
-                                   1, tmC, a);
-  if (e != cudaSuccess) return e;
-  return a.never_cut ? cudaSuccess : launch_cache_join(a, MT, num_sms, s);
+  return launch_dependent(cache_token_kernel<R>, dim3(num_sms), dim3(kThreads), C::SMEM, s, 1, tmC,
+                          a);
 }
 
 }  // namespace
