@@ -107,13 +107,11 @@ cudaError_t launch_cache_attn_tc(const CacheAttn& a, const CUtensorMap& tmC, int
                                  cudaStream_t s);
 cudaError_t launch_cache_mass_tc(const CacheAttn& a, const CUtensorMap& tmC, int num_sms,
                                  cudaStream_t s);
-// Its form for blocks of 16 pairs, and the sum of the blocks that were cut (mt: rows
-// of a block).
+// Their forms for blocks of 16 pairs.
 cudaError_t launch_cache_token(const CacheAttn& a, const CUtensorMap& tmC, int num_sms,
                                cudaStream_t s);
 cudaError_t launch_cache_mass_token(const CacheAttn& a, const CUtensorMap& tmC, int num_sms,
                                     cudaStream_t s);
-cudaError_t launch_cache_join(const CacheAttn& a, int mt, int num_sms, cudaStream_t s);
 constexpr int kCacheBox = 64;              // rows of a box of tmC, or a page if that is smaller
 constexpr int kCacheBlockRows = 128;       // largest block of pairs
 // CUDA-core attention (any rank up to 256, both types) and its accumulation.

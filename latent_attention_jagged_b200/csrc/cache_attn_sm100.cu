@@ -3,19 +3,26 @@
 //   s_it = scale q_i . c_t over the events row i sees,  P = softmax(s),
 //   o_i = sum_t P_it c_t,  lse_i = log sum_t exp(s_it)
 //
-// One item = a block of MT (query row, head) pairs of one user and a run of its
-// tiles of 128 events (cache_sched.cuh); K and V are one shared-memory copy of a
-// tile, K-major for S = Q C^T and MN-major for O += P C, as in attn_sm100.cu.
-// What differs from the batch kernel: a tile is gathered page by page (one TMA
-// box per page and 64 columns, so pages of 16 to 128 rows cost the same bytes),
-// rows hide events behind a window, a block may be cut between CTAs, and what a
-// row does not see may hold any bits.
+// A piece of work = a block of 128 (query row, head) pairs of one user and a run of its
+// tiles of 128 events (cache_sched.cuh); K and V are one shared-memory copy of a tile,
+// K-major for S = Q C^T and MN-major for O += P C, as in attn_sm100.cu.  What differs
+// from the batch kernel: a tile is gathered page by page (one TMA box per page and 64
+// columns, so pages of 16 to 128 rows cost the same bytes), rows hide events behind a
+// window, a block may be cut between CTAs, and what a row does not see may hold any
+// bits.  Few pairs a user (single tokens) run in cache_token_sm100.cu.
 //
-// MT = 128: blocks of many rows (chunks of new events, candidates), bound by the
-// tensor pipe and the exponentials.  MT = 32: few pairs a user (single tokens),
-// bound by reading the cache; the M = 128 products then use a quarter of their
-// lanes, which costs nothing (about 1000 tensor cycles per 64 KB tile, of the 2750
-// that HBM needs for it), the query block is 32 rows, and the ring gets the space.
+// What bounds it: a tile is 1024 (r = 128) or 2048 (r = 256) cycles of the tensor pipe
+// and 1024 of the exponentials, but the chain S -> softmax -> P C of a tile is about
+// 5500 cycles long, and tensor memory (r = 128) or shared memory (r = 256: two tiles
+// beside the queries) holds two tiles at a time.  So a tile is handled in two halves by
+// two of four softmax groups, only the running maximum goes from half to half, and the
+// two issuing warps never wait for each other's operands.  A tile takes about 3800
+// cycles in short blocks (64 candidates for 256 users) and 4000 in long ones (chunks
+// of 500 to 800 events, r = 256).  Measured and dropped: one softmax group per tile
+// (4800 a tile), one thread issuing all products (a divergent lane took 68 cycles per
+// MMA), tiles of 64 events (an N = 64 product runs at 54 cycles for half the work),
+// scores kept in registers instead of read twice (spills at 88 registers; with three
+// groups at 112 the same time).
 //
 // Hidden values.  P = 0 does not hide an infinity or NaN from the product P C, so
 // in tiles where some row hides some event (the tile of the length's end, window
@@ -41,13 +48,15 @@ using namespace tc;
 namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int MT = 128;                   // (row, head) pairs of a block
 constexpr int KT = 128;                   // events of a tile
 constexpr int HT = KT / 2;                // events of a half
 constexpr int NG = 4;                     // softmax groups
 
 // Six warpgroups: producer (warp 0), issuers of S (warp 1) and of P C (warp 2), the
-// planner (warp 3); four of softmax; the epilogue.  The launch's 80 registers a thread are dealt out again: 128 threads x
-// (56 + 4 x 80 + 104) = 768 x 80 (softmax keeps what it has).
+// planner (warp 3); four of softmax; the epilogue.  The launch's 80 registers a thread
+// are dealt out again: 128 threads x (56 + 4 x 80 + 104) = 768 x 80 (softmax keeps what
+// it has).
 constexpr int kThreads = 768;
 constexpr int kRegsIssue = 56, kRegsSoft = 80, kRegsEpi = 104;
 static_assert(kRegsIssue + NG * kRegsSoft + kRegsEpi <= 480, "registers of the launch");
@@ -74,18 +83,15 @@ struct __align__(16) Piece {
 };
 constexpr int NPIECE = 4;
 
-template <int R, int MT>
+template <int R>
 struct Cfg {
-  static constexpr bool SMALL = MT == 32;
   static constexpr int RSUB = R / 64;
-  // Half S buffers: 3 tiles where tensor memory has the room, so that a softmax group
-  // finds its next half ready (with 2 tiles it waits for S after P C of its last one)
-  static constexpr int NS = R == 64 ? 6 : 4;
-  static constexpr int OBUF = 2 * R + NS * HT <= 512 ? 2 : 1;
-  static constexpr int QBUF = SMALL || R <= 128 ? 2 : 1;
-  static constexpr int KS = SMALL ? (R == 256 ? 6 : 12) : (R == 256 ? 4 : R == 128 ? 6 : 12);   // halves in the ring
+  static constexpr int NS = NG;                        // half S buffers
+  static constexpr int OBUF = R <= 128 ? 2 : 1;        // O, over the pieces
+  static constexpr int QBUF = R <= 128 ? 2 : 1;
+  static constexpr int KS = R == 256 ? 4 : R == 128 ? 6 : 12;   // halves in the ring
   // 32 rows x 64 columns of output on their way to global memory, for each quadrant
-  static constexpr int NSTG = SMALL ? 0 : R == 128 ? 2 : 1;
+  static constexpr int NSTG = R == 128 ? 2 : 1;
   static constexpr uint32_t STG_BYTES = 32 * 128;
   static constexpr uint32_t QSUB = MT * 128;           // one 64-wide sub-tile of a query block
   static constexpr uint32_t Q_BYTES = RSUB * QSUB;
@@ -96,15 +102,12 @@ struct Cfg {
   static constexpr uint32_t KV_SUB = KS * H_SUB;
   static_assert(KS % 2 == 0 && KS >= NG, "halves of a tile are neighbours");
   static constexpr uint32_t S_COL = OBUF * R;
-  static constexpr int NQ = SMALL ? 1 : 4;             // TMEM lane quadrants in use
   static constexpr uint32_t BAR_BYTES = 576 + NPIECE * (sizeof(Piece) + 16);
   static constexpr uint32_t F_BYTES = (OBUF * 2 + 1) * NG * MT * 4;   // sums, maxima
   static constexpr size_t SMEM = 1024 + QBUF * Q_BYTES + (size_t)KS * H_BYTES +
                                  4 * NSTG * STG_BYTES + BAR_BYTES + F_BYTES;
   static_assert(SMEM <= 232448, "shared memory budget");
   static_assert(OBUF * R + NS * HT <= 512, "TMEM budget");
-  // an M = 128 product reads 16 KB from the start of a 32-row sub-tile
-  static_assert(!SMALL || KS * H_BYTES >= 16384, "operand reads stay in the buffers");
   // the split works in the ring before its first load
   static_assert(KS * H_BYTES >= sizeof(CacheSplitSpace), "split");
 };
@@ -145,11 +148,11 @@ __device__ __forceinline__ void clear_rows(uint8_t* kv, uint32_t sub) {
   fence_proxy_async_smem();
 }
 
-template <int R, int MT>
+template <int R>
 __global__ void __launch_bounds__(kThreads, 1)
 cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmC,
                   const __grid_constant__ CUtensorMap tmO, const CacheAttn p) {
-  using C = Cfg<R, MT>;
+  using C = Cfg<R>;
   using Line = ByRows<MT, KT>;
   constexpr int RSUB = C::RSUB, KS = C::KS, OBUF = C::OBUF, QBUF = C::QBUF, NS = C::NS;
   extern __shared__ uint8_t smem_raw[];
@@ -190,12 +193,12 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     for (int s = 0; s < 2; ++s) {
       mbar_init(&q_full[s], 1);
       mbar_init(&q_empty[s], 1);
-      mbar_init(&o_full[s], 1 + NG * C::NQ);
-      mbar_init(&o_free[s], C::NQ);
+      mbar_init(&o_full[s], 1 + NG * 4);
+      mbar_init(&o_free[s], 4);
     }
     for (int s = 0; s < NS / 2; ++s) mbar_init(&s_full[s], 1);
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&p_full[s], C::NQ);
+      mbar_init(&p_full[s], 4);
       mbar_init(&p_empty[s], 1);
     }
     for (int s = 0; s < NG; ++s) {
@@ -204,7 +207,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     for (int s = 0; s < KS; ++s) { mbar_init(&kv_full[s], 1); mbar_init(&kv_empty[s], 1); }
     for (int s = 0; s < NPIECE; ++s) {
       mbar_init(&piece_full[s], 1);
-      mbar_init(&piece_empty[s], 3 + (NG + 1) * C::NQ);
+      mbar_init(&piece_empty[s], 3 + 4 * (NG + 1));   // the warps that take it
     }
     mbar_init(drain, 1);
     mbar_init(drain + 1, 1);
@@ -241,184 +244,184 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   };
 
   if (warp < 4) {
-  regs_down<kRegsIssue>();
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    // Lane l < boxes of half a tile gathers box l, a page or, of a larger page, a part; events that no row of the block sees, and pages outside the pool, read
-    // as zeros (a box past the pool's last row).
-    uint32_t itm = 0, g = 0, qi = 0;
-    const int32_t P = min(1 << c.page_shift, kCacheBox);     // events of a box
-    const int np = HT / P;
-    const int32_t outside = c.n_pages << c.page_shift;
-    Piece it;
-    bool ok = true;
-    while (ok && take(it)) {
-      const CacheBlock& blk = it.k;
-      if (it.len == 0) continue;
-      const int32_t* row = c.table + (int64_t)it.u * c.stride;
-      // pool row of this lane's box in half h of the piece's tiles
-      auto place = [&](int h) -> int32_t {
-        const int32_t t = cache_tile(blk, h >> 1) * KT + (h & 1) * HT + lane * P;
-        if (lane >= np || !cache_seen(c, blk, t, t + P)) return outside;
-        const int32_t page = __ldg(row + (t >> c.page_shift));
-        if ((uint32_t)page < (uint32_t)c.n_pages)
-          return (page << c.page_shift) + (t & ((1 << c.page_shift) - 1));
-        atomicOr(c.status, LLATTE_DEV_BAD_ID);
-        return outside;
-      };
-      int32_t y = place(2 * it.t0);
-      const int qb = itm % QBUF;
-      if (lane == 0) {
-        ok = mbar_wait(&q_empty[qb], ((itm / QBUF) & 1) ^ 1, abort_flag, c.status);
-        if (ok) {
-          mbar_arrive_expect_tx(&q_full[qb], C::Q_BYTES);
-          const int32_t qrow = (int32_t)it.at0;
-#pragma unroll
-          for (int s = 0; s < RSUB; ++s)
-            tma_load_2d(&tmQ, &q_full[qb], sQ + qb * C::Q_BYTES + s * C::QSUB, s * 64, qrow);
-          ++qi;
-        }
-      }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
-      for (int i = 2 * it.t0; i < 2 * it.t1; ++i, ++g) {
-        const int32_t y_next = i + 1 < 2 * it.t1 ? place(i + 1) : 0;
-        const int st = g % KS;
+    regs_down<kRegsIssue>();
+    if (warp == 0) {
+      // ------------------------------------------------------------ producer
+      // Lane l < boxes of half a tile gathers box l, a page or, of a larger page, a
+      // part; events that no row of the block sees, and pages outside the pool, read as
+      // zeros (a box past the pool's last row).
+      uint32_t itm = 0, g = 0, qi = 0;
+      const int32_t P = min(1 << c.page_shift, kCacheBox);     // events of a box
+      const int np = HT / P;
+      const int32_t outside = c.n_pages << c.page_shift;
+      Piece it;
+      bool ok = true;
+      while (ok && take(it)) {
+        const CacheBlock& blk = it.k;
+        if (it.len == 0) continue;
+        const int32_t* row = c.table + (int64_t)it.u * c.stride;
+        // pool row of this lane's box in half h of the piece's tiles
+        auto place = [&](int h) -> int32_t {
+          const int32_t t = cache_tile(blk, h >> 1) * KT + (h & 1) * HT + lane * P;
+          if (lane >= np || !cache_seen(c, blk, t, t + P)) return outside;
+          const int32_t page = __ldg(row + (t >> c.page_shift));
+          if ((uint32_t)page < (uint32_t)c.n_pages)
+            return (page << c.page_shift) + (t & ((1 << c.page_shift) - 1));
+          atomicOr(c.status, LLATTE_DEV_BAD_ID);
+          return outside;
+        };
+        int32_t y = place(2 * it.t0);
+        const int qb = itm % QBUF;
         if (lane == 0) {
-          ok = mbar_wait(&kv_empty[st], ((g / KS) & 1) ^ 1, abort_flag, c.status);
-          if (ok) mbar_arrive_expect_tx(&kv_full[st], C::H_BYTES);
+          ok = mbar_wait(&q_empty[qb], ((itm / QBUF) & 1) ^ 1, abort_flag, c.status);
+          if (ok) {
+            mbar_arrive_expect_tx(&q_full[qb], C::Q_BYTES);
+            const int32_t qrow = (int32_t)it.at0;
+#pragma unroll
+            for (int s = 0; s < RSUB; ++s)
+              tma_load_2d(&tmQ, &q_full[qb], sQ + qb * C::Q_BYTES + s * C::QSUB, s * 64, qrow);
+            ++qi;
+          }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
-        if (lane < np) {
-          uint8_t* dst = sKV + st * C::H_SUB + lane * P * 128;
+        for (int i = 2 * it.t0; i < 2 * it.t1; ++i, ++g) {
+          const int32_t y_next = i + 1 < 2 * it.t1 ? place(i + 1) : 0;
+          const int st = g % KS;
+          if (lane == 0) {
+            ok = mbar_wait(&kv_empty[st], ((g / KS) & 1) ^ 1, abort_flag, c.status);
+            if (ok) mbar_arrive_expect_tx(&kv_full[st], C::H_BYTES);
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
+          if (lane < np) {
+            uint8_t* dst = sKV + st * C::H_SUB + lane * P * 128;
 #pragma unroll
-          for (int s = 0; s < RSUB; ++s)
-            tma_load_2d(&tmC, &kv_full[st], dst + s * C::KV_SUB, s * 64, y);
+            for (int s = 0; s < RSUB; ++s)
+              tma_load_2d(&tmC, &kv_full[st], dst + s * C::KV_SUB, s * 64, y);
+          }
+          y = y_next;
         }
-        y = y_next;
-      }
-      ++itm;
-    }
-    __syncwarp();
-    // after an abort the MMA thread may have left tiles unread
-    if (lane == 0 && *abort_flag) {
-      drain_ring(kv_full, KS, g, c.status);
-      drain_ring(q_full, QBUF, qi, c.status);
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ S = Q C^T
-    // Two warps issue, so that neither a tile on its way from memory nor a softmax
-    // holds up the other's products.  Both stay converged and one lane issues:
-    // descriptors then live in uniform registers (from one divergent lane an MMA took
-    // 68 cycles to issue, more than it takes to run).
-    constexpr uint32_t IDESC_S = idesc_bf16(128, KT, false, false);
-    const bool elect = elect_one();
-    uint32_t itm = 0, g = 0;               // items, tiles
-    bool ok = true;
-    Piece it;
-    while (ok && take(it)) {
-      if (it.len == 0) continue;
-      const int qb = itm % QBUF;
-      if (!warp_wait(&q_full[qb], (itm / QBUF) & 1, abort_flag, c.status)) break;
-      const uint64_t ad = sdesc_sw128(smem_u32(sQ + qb * C::Q_BYTES), 16, 1024);
-      for (int i = it.t0; i < it.t1; ++i, ++g) {
-        const int st = (2 * g) % KS, sb = g % (NS / 2);
-        // both halves are here; the products that read P in this S buffer are done
-        ok = warp_wait(&kv_full[st], (2 * g / KS) & 1, abort_flag, c.status) &&
-             warp_wait(&kv_full[st + 1], (2 * g / KS) & 1, abort_flag, c.status) &&
-             warp_wait(&p_empty[2 * sb + 1], ((g / (NS / 2)) & 1) ^ 1, abort_flag, c.status);
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t bd = sdesc_sw128(smem_u32(sKV + st * C::H_SUB), 16, 1024);
-        const uint32_t d = tmem + C::S_COL + sb * KT;
-        const bool last = i == it.t1 - 1;
-        if (elect) {
-#pragma unroll
-          for (int k = 0; k < R / 16; ++k)
-            umma_bf16(d, ad + (((k >> 2) * C::QSUB + (k & 3) * 32) >> 4),
-                      bd + (((k >> 2) * C::KV_SUB + (k & 3) * 32) >> 4), IDESC_S, k > 0 ? 1u : 0u);
-          umma_commit(&s_full[sb]);
-          if (last) umma_commit(&q_empty[qb]);
-        }
-        __syncwarp();
-      }
-      ++itm;
-    }
-    if (elect) umma_commit(drain);
-    __syncwarp();
-    int dummy = 0;
-    mbar_wait(drain, 0, &dummy, c.status);
-    __syncwarp();
-  } else if (warp == 2) {
-    // ------------------------------------------------------------ O += P C
-    // P from TMEM, half a tile read MN-major; the first half of an item starts O anew.
-    constexpr uint32_t IDESC_O = idesc_bf16(128, R, false, true);
-    const bool elect = elect_one();
-    uint32_t itm = 0, g = 0;               // items, halves
-    bool ok = true;
-    Piece it;
-    while (ok && take(it)) {
-      if (it.len == 0) continue;
-      const int ob = itm % OBUF;
-      if (!warp_wait(&o_free[ob], ((itm / OBUF) & 1) ^ 1, abort_flag, c.status)) break;
-      for (int i = 2 * it.t0; i < 2 * it.t1; ++i, ++g) {
-        const int st = g % KS, sb = g % NS;
-        ok = warp_wait(&p_full[sb], (g / NS) & 1, abort_flag, c.status);
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t bd = sdesc_sw128(smem_u32(sKV + st * C::H_SUB), C::KV_SUB, 1024);
-        const uint32_t p_tmem = tmem + C::S_COL + sb * HT;
-        const bool first = i == 2 * it.t0, last = i == 2 * it.t1 - 1;
-        if (elect) {
-#pragma unroll
-          for (int k = 0; k < HT / 16; ++k)
-            umma_bf16_ts(tmem + ob * R, p_tmem + k * 8, bd + (k * 2048 >> 4), IDESC_O,
-                         (!first || k > 0) ? 1u : 0u);
-          umma_commit(&kv_empty[st]);
-          umma_commit(&p_empty[sb]);
-          if (last) umma_commit(&o_full[ob]);
-        }
-        __syncwarp();
-      }
-      ++itm;
-    }
-    if (elect) umma_commit(drain + 1);
-    __syncwarp();
-    int dummy = 0;
-    mbar_wait(drain + 1, 0, &dummy, c.status);
-    __syncwarp();
-  } else {
-    // ------------------------------------------------------------ planner
-    CacheItems<Line> items;
-    items.start(c, run);
-    CacheItem<Line> it;
-    uint32_t n = 0;
-    for (bool more = true; more; ++n) {
-      more = items.next(c, it);
-      const int st = n % NPIECE;
-      if (!warp_wait(&piece_empty[st], ((n / NPIECE) & 1) ^ 1, abort_flag, c.status)) break;
-      if (lane == 0) {
-        Piece q = {};
-        q.u = -1;
-        if (more) {
-          q.u = it.u;
-          q.pair0 = it.b * MT;
-          q.at0 = it.x.row0 * c.heads + q.pair0;
-          q.rows = (int32_t)min((uint32_t)MT, (uint32_t)it.x.n * (uint32_t)c.heads - q.pair0);
-          q.m = it.x.m; q.len = it.x.len;
-          q.t0 = it.t0; q.t1 = it.t1; q.k = it.k;
-          q.parts = it.parts; q.whole = it.whole; q.starts = it.starts;
-        }
-        pieces[st] = q;
-        mbar_arrive(&piece_full[st]);
+        ++itm;
       }
       __syncwarp();
+      // after an abort the MMA thread may have left tiles unread
+      if (lane == 0 && *abort_flag) {
+        drain_ring(kv_full, KS, g, c.status);
+        drain_ring(q_full, QBUF, qi, c.status);
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ S = Q C^T
+      // Two warps issue, so that neither a tile on its way from memory nor a softmax
+      // holds up the other's products.  Both stay converged and one lane issues:
+      // descriptors then live in uniform registers (from one divergent lane an MMA took
+      // 68 cycles to issue, more than it takes to run).
+      constexpr uint32_t IDESC_S = idesc_bf16(128, KT, false, false);
+      const bool elect = elect_one();
+      uint32_t itm = 0, g = 0;               // items, tiles
+      bool ok = true;
+      Piece it;
+      while (ok && take(it)) {
+        if (it.len == 0) continue;
+        const int qb = itm % QBUF;
+        if (!warp_wait(&q_full[qb], (itm / QBUF) & 1, abort_flag, c.status)) break;
+        const uint64_t ad = sdesc_sw128(smem_u32(sQ + qb * C::Q_BYTES), 16, 1024);
+        for (int i = it.t0; i < it.t1; ++i, ++g) {
+          const int st = (2 * g) % KS, sb = g % (NS / 2);
+          // both halves are here; the products that read P in this S buffer are done
+          ok = warp_wait(&kv_full[st], (2 * g / KS) & 1, abort_flag, c.status) &&
+               warp_wait(&kv_full[st + 1], (2 * g / KS) & 1, abort_flag, c.status) &&
+               warp_wait(&p_empty[2 * sb + 1], ((g / (NS / 2)) & 1) ^ 1, abort_flag, c.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t bd = sdesc_sw128(smem_u32(sKV + st * C::H_SUB), 16, 1024);
+          const uint32_t d = tmem + C::S_COL + sb * KT;
+          const bool last = i == it.t1 - 1;
+          if (elect) {
+#pragma unroll
+            for (int k = 0; k < R / 16; ++k)
+              umma_bf16(d, ad + (((k >> 2) * C::QSUB + (k & 3) * 32) >> 4),
+                        bd + (((k >> 2) * C::KV_SUB + (k & 3) * 32) >> 4), IDESC_S, k > 0 ? 1u : 0u);
+            umma_commit(&s_full[sb]);
+            if (last) umma_commit(&q_empty[qb]);
+          }
+          __syncwarp();
+        }
+        ++itm;
+      }
+      if (elect) umma_commit(drain);
+      __syncwarp();
+      int dummy = 0;
+      mbar_wait(drain, 0, &dummy, c.status);
+      __syncwarp();
+    } else if (warp == 2) {
+      // ------------------------------------------------------------ O += P C
+      // P from TMEM, half a tile read MN-major; the first half of an item starts O anew.
+      constexpr uint32_t IDESC_O = idesc_bf16(128, R, false, true);
+      const bool elect = elect_one();
+      uint32_t itm = 0, g = 0;               // items, halves
+      bool ok = true;
+      Piece it;
+      while (ok && take(it)) {
+        if (it.len == 0) continue;
+        const int ob = itm % OBUF;
+        if (!warp_wait(&o_free[ob], ((itm / OBUF) & 1) ^ 1, abort_flag, c.status)) break;
+        for (int i = 2 * it.t0; i < 2 * it.t1; ++i, ++g) {
+          const int st = g % KS, sb = g % NS;
+          ok = warp_wait(&p_full[sb], (g / NS) & 1, abort_flag, c.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t bd = sdesc_sw128(smem_u32(sKV + st * C::H_SUB), C::KV_SUB, 1024);
+          const uint32_t p_tmem = tmem + C::S_COL + sb * HT;
+          const bool first = i == 2 * it.t0, last = i == 2 * it.t1 - 1;
+          if (elect) {
+#pragma unroll
+            for (int k = 0; k < HT / 16; ++k)
+              umma_bf16_ts(tmem + ob * R, p_tmem + k * 8, bd + (k * 2048 >> 4), IDESC_O,
+                           (!first || k > 0) ? 1u : 0u);
+            umma_commit(&kv_empty[st]);
+            umma_commit(&p_empty[sb]);
+            if (last) umma_commit(&o_full[ob]);
+          }
+          __syncwarp();
+        }
+        ++itm;
+      }
+      if (elect) umma_commit(drain + 1);
+      __syncwarp();
+      int dummy = 0;
+      mbar_wait(drain + 1, 0, &dummy, c.status);
+      __syncwarp();
+    } else {
+      // ------------------------------------------------------------ planner
+      CacheItems<Line> items;
+      items.start(c, run);
+      CacheItem<Line> it;
+      uint32_t n = 0;
+      for (bool more = true; more; ++n) {
+        more = items.next(c, it);
+        const int st = n % NPIECE;
+        if (!warp_wait(&piece_empty[st], ((n / NPIECE) & 1) ^ 1, abort_flag, c.status)) break;
+        if (lane == 0) {
+          Piece q = {};
+          q.u = -1;
+          if (more) {
+            q.u = it.u;
+            q.pair0 = it.b * MT;
+            q.at0 = it.x.row0 * c.heads + q.pair0;
+            q.rows = (int32_t)min((uint32_t)MT, (uint32_t)it.x.n * (uint32_t)c.heads - q.pair0);
+            q.m = it.x.m; q.len = it.x.len;
+            q.t0 = it.t0; q.t1 = it.t1; q.k = it.k;
+            q.parts = it.parts; q.whole = it.whole; q.starts = it.starts;
+          }
+          pieces[st] = q;
+          mbar_arrive(&piece_full[st]);
+        }
+        __syncwarp();
+      }
     }
-  }
   } else if (warp < 20) {
-  if (quad < C::NQ) {
     // ------------------------------------------------------------ softmax
     // The groups take the halves in turn, group g % NG half g; a thread owns a
     // row.  Only the running maximum goes from one group to the next,
@@ -590,10 +593,8 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       if (lane == 0) mbar_arrive(&o_full[ob]);
       ++itm;
     }
-  }
   } else {
-  regs_up<kRegsEpi>();
-  if (quad < C::NQ) {
+    regs_up<kRegsEpi>();
     // ------------------------------------------------------------ epilogue
     const int row = quad * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
@@ -604,7 +605,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     Piece it;
     while (take(it)) {
       const bool valid = row < it.rows;
-      const bool box = C::NSTG > 0 && quad * 32 + 32 <= it.rows;
+      const bool box = quad * 32 + 32 <= it.rows;
       const bool idle = quad * 32 >= it.rows;
       const int64_t at = it.at0 + row;
       __nv_bfloat16* orow = (__nv_bfloat16*)p.out + at * R;
@@ -637,9 +638,9 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             // as it has been read (64 stores of a lane's own row cost 3500 cycles)
 #pragma unroll 1
             for (int k = 0; k < R; k += 64, ++stg) {
-              uint8_t* buf = sStage + (quad * C::NSTG + stg % max(C::NSTG, 1)) * C::STG_BYTES;
+              uint8_t* buf = sStage + (quad * C::NSTG + stg % C::NSTG) * C::STG_BYTES;
               if (lane == 0)
-                asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(C::NSTG > 0 ? C::NSTG - 1 : 0)
+                asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(C::NSTG - 1)
                              : "memory");
               __syncwarp();
 #pragma unroll
@@ -713,7 +714,6 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     if (lane == 0) tma_store_wait_all();
     __syncwarp();
   }
-  }
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
@@ -725,7 +725,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
 // and did not finish: out = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p, part by
 // part in the order of the events.  One warp per row.
 template <int R>
-__global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttn p, const int mt) {
+__global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttn p) {
   pdl_trigger();
   pdl_wait();
   const CacheJoin j = p.join[blockIdx.x];
@@ -734,7 +734,7 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttn p, cons
   if (row >= j.rows) return;
   // part 0 is the beginning CTA's second slot, the others the first slots
   auto slot = [&](int i) -> int64_t {
-    return ((int64_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * mt + row;
+    return ((int64_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * MT + row;
   };
   float m = -INFINITY;
   for (int i = lane; i < j.parts; i += 32) m = fmaxf(m, p.part_ml[slot(i)].x);
@@ -774,56 +774,46 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttn p, cons
   }
 }
 
-template <int R, int MT>
-cudaError_t launch_rm(const CacheAttn& a, const CUtensorMap& tmC, int num_sms, cudaStream_t s) {
-  using C = Cfg<R, MT>;
+template <int R>
+cudaError_t launch_r(CacheAttn a, const CUtensorMap& tmC, int num_sms, cudaStream_t s) {
+  using C = Cfg<R>;
+  // Blocks of up to 4 tiles are not cut: the tiles that a CTA may have too many of
+  // take less time than the launch that would join the parts.
+  a.min_quota = 1;
+  a.never_cut = cache_most_tiles(a.c, MT, KT) <= 4;
+  // Few pairs a user on average: cache_token_sm100.cu.  Measured at 4 to 16 pairs, r = 128
+  // (400 and 2000 events): 17 to 23 us there, 23 to 25 here; at 32 pairs 29 to 32 there.
+  // At r = 256 its blocks cost more to begin and end, so that many short histories (8
+  // pairs, 200 events, 256 users) take 35 us there and 27 here; 1000 events: 37 and 39.
+  const bool many_short = R == 256 && a.never_cut && a.c.B > num_sms;
+  if (a.pairs <= 16 * (int64_t)a.c.B && !many_short)
+    return launch_cache_token(a, tmC, num_sms, s);
   static uint64_t attr_devices = 0;
   int dev = 0;
   cudaGetDevice(&dev);
   if (!(attr_devices >> (dev & 63) & 1)) {
-    cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<R, MT>,
+    cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<R>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
     if (e != cudaSuccess) return e;
     // the register split waits for what the launch does not have
     cudaFuncAttributes f;
-    e = cudaFuncGetAttributes(&f, cache_attn_kernel<R, MT>);
+    e = cudaFuncGetAttributes(&f, cache_attn_kernel<R>);
     if (e != cudaSuccess) return e;
-    if (f.numRegs * 6 < kRegsIssue + NG * kRegsSoft + kRegsEpi) return cudaErrorInvalidConfiguration;
+    if (f.numRegs * (kThreads / 128) < kRegsIssue + NG * kRegsSoft + kRegsEpi)
+      return cudaErrorInvalidConfiguration;
     attr_devices |= 1ull << (dev & 63);
   }
   CUtensorMap tmQ, tmO;
   const uint64_t pairs = (uint64_t)a.c.rows * a.c.heads;
   if (!make_tmap_bf16(&tmQ, a.q, pairs, R, MT) || !make_tmap_bf16(&tmO, a.out, pairs, R, 32))
     return cudaErrorInvalidValue;
-  cudaError_t e = launch_dependent(cache_attn_kernel<R, MT>, dim3(num_sms), dim3(kThreads),
-                                   C::SMEM, s, 1, tmQ, tmC, tmO, a);
-  if (e != cudaSuccess) return e;
-  return a.never_cut ? cudaSuccess : launch_cache_join(a, MT, num_sms, s);
-}
-
-template <int R>
-cudaError_t launch_r(CacheAttn a, const CUtensorMap& tmC, int num_sms, cudaStream_t s) {
-  // Blocks of up to 4 tiles are not cut: the tiles that a CTA may have too many of
-  // take less time than the launch that would join the parts.
-  a.min_quota = 1;
-  a.never_cut = cache_most_tiles(a.c, 128, KT) <= 4;
-  // few pairs a user on average: see cache_token_sm100.cu
-  if (a.pairs <= 16 * (int64_t)a.c.B) return launch_cache_token(a, tmC, num_sms, s);
-
-  return launch_rm<R, 128>(a, tmC, num_sms, s);
+  const cudaError_t e = launch_dependent(cache_attn_kernel<R>, dim3(num_sms), dim3(kThreads), C::SMEM,
+                                         s, 1, tmQ, tmC, tmO, a);
+  if (e != cudaSuccess || a.never_cut) return e;
+  return launch_dependent(cache_join_kernel<R>, dim3(num_sms, MT / 8), dim3(256), 0, s, 1, a);
 }
 
 }  // namespace
-
-cudaError_t launch_cache_join(const CacheAttn& a, int mt, int num_sms, cudaStream_t s) {
-  const dim3 grid(num_sms, mt / 8);
-  switch (a.c.r) {
-    case 64: return launch_dependent(cache_join_kernel<64>, grid, dim3(256), 0, s, 1, a, mt);
-    case 128: return launch_dependent(cache_join_kernel<128>, grid, dim3(256), 0, s, 1, a, mt);
-    case 256: return launch_dependent(cache_join_kernel<256>, grid, dim3(256), 0, s, 1, a, mt);
-    default: return cudaErrorInvalidValue;
-  }
-}
 
 bool cache_attn_tc_supported(int r) { return r == 64 || r == 128 || r == 256; }
 

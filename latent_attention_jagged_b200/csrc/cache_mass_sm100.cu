@@ -353,6 +353,7 @@ cudaError_t launch_rn(const CacheAttn& a, const CUtensorMap& tmC, int num_sms, c
 
 template <int R>
 cudaError_t launch_r(const CacheAttn& a, const CUtensorMap& tmC, int num_sms, cudaStream_t s) {
+  // few pairs a user: 27 us there, 34 us here (128 users, 8 pairs, 800 to 1600 events)
   if (a.pairs <= 16 * (int64_t)a.c.B)
     return launch_cache_mass_token(a, tmC, num_sms, s);
   return launch_rn<R>(a, tmC, num_sms, s);
