@@ -509,7 +509,7 @@ bool cache_uses_tc(const llatte_cache_dims& d) {
   return d.dtype == LLATTE_BF16 && cache_attn_tc_supported(d.rank);
 }
 
-struct CacheLayout { size_t status, count, list, lse2, part_o, part_ml, join, parts, total; };
+struct CacheLayout { size_t status, count, list, lse2, part_o, part_ml, join, parts, zeros, total; };
 
 // The parts' slots are counted for the largest part there is (148 SMs); a device
 // with more SMs runs as many CTAs as there are slots.
@@ -519,15 +519,17 @@ CacheLayout cache_layout(const llatte_cache_dims& d) {
   CacheLayout L = {};
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t r = o; o += align_up(bytes); return r; };
+  // first what starts as zeros
   L.status = take(sizeof(int32_t));
+  L.join = take(sizeof(CacheJoin) * kCacheCtas);
+  L.parts = take(sizeof(int32_t) * kCacheCtas);
+  L.zeros = o;
   L.count = take(sizeof(int32_t) * d.max_batch);
   L.list = take(sizeof(int32_t) * (size_t)d.max_batch * d.max_pages * d.page_size);
   L.lse2 = take(sizeof(float) * (size_t)d.max_rows * d.heads);
   const size_t slots = (size_t)2 * kCacheCtas * (cache_uses_tc(d) ? kCacheBlockRows : 64);
   L.part_o = take(sizeof(float) * slots * d.rank);
   L.part_ml = take(sizeof(float2) * slots);
-  L.join = take(sizeof(CacheJoin) * kCacheCtas);
-  L.parts = take(sizeof(int32_t) * kCacheCtas);
   L.total = o;
   return L;
 }
@@ -682,7 +684,7 @@ int llatte_cache_create(llatte_cache** out, const llatte_cache_dims* dims, void*
       return LLATTE_ERR_CUDA;
     }
   }
-  if (cudaMemset(h->ws, 0, L.total) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
+  if (cudaMemset(h->ws, 0, L.zeros) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
     llatte_cache_destroy(h);
     return LLATTE_ERR_CUDA;
   }

@@ -224,7 +224,7 @@ cache_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     CacheJoin* join = p.join + blockIdx.x;
     const bool writer = warp == kSoft0 && lane == 0;
     if (writer) join->rows = 0;
-    uint32_t qn = 0, pphase = 0;
+    uint32_t qn = 0, done = 0, pphase = 0;   // blocks, and those before this piece
     bool ok = true;
     CacheItems<Line> items;
     items.start(c, run);
@@ -236,21 +236,31 @@ cache_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       const uint32_t pairs = (uint32_t)it.x.n * (uint32_t)c.heads;
       // the first events are inside every window
       const int32_t tw = t < c.n_sink ? INT32_MAX : t;
-      float sum = 0.f;
-      for (int i = it.t0; i < it.t1; ++i, ++qn) {
-        if ((int)(qn & 1) != group) continue;
+      // log sums of this lane's two pairs of block i
+      const float* lse = p.lse2 + it.x.row0 * c.heads;
+      auto pair_of = [&](int i, int k) -> uint32_t {
+        return (uint32_t)(it.k.first + i) * NP + part * CP + lane + 32 * k;
+      };
+      auto ask = [&](int i, float (&v)[2]) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) v[k] = i < it.t1 && pair_of(i, k) < pairs ? lse[pair_of(i, k)] : 0.f;
+      };
+      float sum = 0.f, next[2];
+      const int i0 = it.t0 + (int)((qn ^ group) & 1);      // this group's first block
+      qn += i0 - it.t0;
+      ask(i0, next);
+      for (int i = i0; i < it.t1; i += 2, qn += 2) {
         const int sb = qn % SB;
-        const uint32_t pair0 = (uint32_t)(it.k.first + i) * NP + part * CP;
         __syncwarp();
 #pragma unroll
-        for (int k = lane; k < CP; k += 32) {
-          const uint32_t pair = pair0 + k;
-          const bool in = pair < pairs;
-          const int32_t pos = in ? cache_pos(it.x, cache_div(c, pair)) : -1;
-          lw[k] = in ? p.lse2[it.x.row0 * c.heads + pair] : 0.f;
-          pw[k] = pos;
-          ww[k] = cache_low(c, pos);
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t pair = pair_of(i, k);
+          const int32_t pos = pair < pairs ? cache_pos(it.x, cache_div(c, pair)) : -1;
+          lw[lane + 32 * k] = next[k];
+          pw[lane + 32 * k] = pos;
+          ww[lane + 32 * k] = cache_low(c, pos);
         }
+        ask(i + 2, next);                  // on its way while this block is summed
         __syncwarp();
         bool w = mbar_wait(&s_full[sb], (qn / SB) & 1, abort_flag, c.status);
         if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
@@ -282,6 +292,8 @@ cache_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
       }
       if (!ok) break;
+      qn = done + (uint32_t)(it.t1 - it.t0);
+      done = qn;
       // the groups' halves of the pairs meet, in this order
       const int lead = group * 2 + part;
       if (lead) sums[(lead - 1) * 128 + quad * 32 + lane] = sum;

@@ -146,6 +146,7 @@ __device__ __forceinline__ void cache_cut(const CacheCall& c, const CacheSplitSp
   // the last user whose places start at or before the cut (skips empty users): a
   // 32-way search
   int lo = 0, n = c.B;                      // it is one of n users from lo
+#pragma unroll 1
   while (n > 1) {
     const int step = (n + 31) / 32, i = lo + lane * step;
     const uint32_t le = __ballot_sync(0xffffffffu, lane * step < n && w.prefix[min(i, c.B)] <= at);
@@ -159,6 +160,7 @@ __device__ __forceinline__ void cache_cut(const CacheCall& c, const CacheSplitSp
   s->x = x;
   const int nb = W::blocks(c, x);
   int32_t left = (int32_t)at - w.prefix[lo];
+#pragma unroll 1
   for (int b0 = 0; b0 < nb; b0 += 32) {
     const int b = b0 + lane;
     const int32_t own = b < nb ? W::places(W::block(c, x, b)) : 0;
@@ -197,11 +199,13 @@ __device__ __forceinline__ void cache_split(const CacheCall& c, int min_quota, b
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   constexpr int64_t kTop = (int64_t)1 << 31;
   bool many = false, too_many = false;
+#pragma unroll 1
   for (int u = threadIdx.x; u < c.B; u += blockDim.x) {
     const CacheUser x = cache_user(c, u);
     const int nb = W::blocks(c, x);
     int64_t places = 0;
     if (nb <= 4) {
+#pragma unroll 1
       for (int b = 0; b < nb; ++b) places += W::places(W::block(c, x, b));
     } else {
       many = true;
@@ -219,6 +223,7 @@ __device__ __forceinline__ void cache_split(const CacheCall& c, int min_quota, b
       const CacheUser x = {0, d.x, max(0, d.x - c.n_cand), d.y};
       const int nb = W::blocks(c, x);
       int64_t sum = 0;
+#pragma unroll 1
       for (int b = lane; b < nb; b += 32) sum += W::places(W::block(c, x, b));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -232,6 +237,7 @@ __device__ __forceinline__ void cache_split(const CacheCall& c, int min_quota, b
   if (warp < 2) {
     const int per = (c.B + 31) / 32, u0 = min(lane * per, c.B), u1 = min(u0 + per, c.B);
     int64_t v = 0;
+#pragma unroll 1
     for (int u = u0; u < u1; ++u) v += w.prefix[u + 1];
     int64_t incl = v;
 #pragma unroll
@@ -247,6 +253,7 @@ __device__ __forceinline__ void cache_split(const CacheCall& c, int min_quota, b
     asm volatile("bar.sync 1, 64;" ::: "memory");       // both have read the places
     if (warp == 0) {
       int64_t sum = incl - v;
+#pragma unroll 1
       for (int u = u0; u < u1; ++u) {
         sum += w.prefix[u + 1];
         w.prefix[u + 1] = (int32_t)min(sum, kTop - 1);
