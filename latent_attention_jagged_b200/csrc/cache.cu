@@ -29,8 +29,8 @@ struct llatte_cache {
   CUtensorMap tmC;       // the pool, a page a box (tc)
   float* part_o;         // [2 num_sms, block rows, rank]
   float2* part_ml;       // [2 num_sms, block rows]
-  CacheJoin* join;       // [num_sms]
-  int32_t* parts;        // [num_sms]
+  CacheJoin* join;       // [2 num_sms]
+  int32_t* parts;        // [2 num_sms]
 };
 
 namespace llatte {
@@ -38,13 +38,14 @@ namespace {
 
 // ---------------------------------------------------------------- append
 // c = x / sqrt(mean(x^2) + eps) * g.  Bound by reading and writing the rows; what a row
-// waits for is its place (offsets -> user -> length, page).  So a warp takes 4 steps
+// waits for is its place (offsets -> user -> length, page).  So a warp takes STEPS steps
 // of 32 / G rows (G lanes a row, NV 16-byte vectors a lane), asks for all of them
 // before it looks for their users, and one lane per row finds the place: a 32-way
 // search by the warp for its first and last row, the rest between the two.
-template <typename T, int G, int NV>
+template <typename T, int G, int NV, int STEPS>
 __global__ void __launch_bounds__(256) cache_append_kernel(CacheAppend a) {
-  constexpr int EV = 16 / sizeof(T), STEP = 32 / G, ROWS = 4 * STEP;
+  constexpr int EV = 16 / sizeof(T), STEP = 32 / G, ROWS = STEPS * STEP;
+  static_assert(ROWS <= 32, "one lane finds the place of a row");
   const CacheCall& c = a.c;
   const int lane = threadIdx.x & 31;
   const int64_t row0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * ROWS;
@@ -53,9 +54,9 @@ __global__ void __launch_bounds__(256) cache_append_kernel(CacheAppend a) {
     for (int u = threadIdx.x; u < c.B; u += 256) cache_user(c, u);
   if (row0 >= min(c.rows, __ldg(c.qoff + c.B))) return;
   const int nvec = c.r / EV, sub = lane / G, k0 = lane % G;
-  uint4 v[4][NV];
+  uint4 v[STEPS][NV];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < STEPS; ++i)
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int64_t row = row0 + i * STEP + sub;
@@ -102,7 +103,7 @@ __global__ void __launch_bounds__(256) cache_append_kernel(CacheAppend a) {
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < STEPS; ++i) {
     const int64_t to = __shfl_sync(0xffffffffu, dst, i * STEP + sub);
     if (a.gain) {
       float ss = 0.f;
@@ -444,11 +445,24 @@ cache_copy_kernel(CacheEvict a, int nvec) {
   }
 }
 
+template <typename T, int G, int NV, int STEPS>
+cudaError_t append_s(const CacheAppend& a, cudaStream_t s) {
+  constexpr int rows = 8 * STEPS * 32 / G;
+  cache_append_kernel<T, G, NV, STEPS>
+      <<<(unsigned)((a.c.rows + rows - 1) / rows), 256, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+// A block lives as long as its chain of loads, whatever it moves: with more rows than one
+// round of blocks of 4 steps takes (4 blocks an SM), 8 steps (256 users of 100 to
+// 400 events, r = 128: 10.2 us with 4, 9.6 with 8).
 template <typename T, int G, int NV>
 cudaError_t append_g(const CacheAppend& a, cudaStream_t s) {
-  constexpr int rows = 8 * 4 * 32 / G;
-  cache_append_kernel<T, G, NV><<<(unsigned)((a.c.rows + rows - 1) / rows), 256, 0, s>>>(a);
-  return cudaGetLastError();
+  constexpr bool more = NV == 1 && G >= 8;
+  if constexpr (more) {
+    if (a.c.rows > (int64_t)592 * 8 * 4 * 32 / G) return append_s<T, G, NV, 8>(a, s);
+  }
+  return append_s<T, G, NV, 4>(a, s);
 }
 
 template <typename T>
@@ -525,13 +539,15 @@ CacheLayout cache_layout(const llatte_cache_dims& d) {
   auto take = [&](size_t bytes) { size_t r = o; o += align_up(bytes); return r; };
   // first what starts as zeros
   L.status = take(sizeof(int32_t));
-  L.join = take(sizeof(CacheJoin) * kCacheCtas);
-  L.parts = take(sizeof(int32_t) * kCacheCtas);
+  L.join = take(sizeof(CacheJoin) * 2 * kCacheCtas);
+  L.parts = take(sizeof(int32_t) * 2 * kCacheCtas);
   L.zeros = o;
   L.count = take(sizeof(int32_t) * d.max_batch);
   L.list = take(sizeof(int32_t) * (size_t)d.max_batch * d.max_pages * d.page_size);
   L.lse2 = take(sizeof(float) * (size_t)d.max_rows * d.heads);
-  const size_t slots = (size_t)2 * kCacheCtas * (cache_uses_tc(d) ? kCacheBlockRows : 64);
+  // two slots a CTA: blocks of kCacheBlockRows, or of 64 for up to two CTAs an SM
+  const size_t slots = (size_t)2 * kCacheCtas * 128;
+  static_assert(kCacheBlockRows == 128, "slots");
   L.part_o = take(sizeof(float) * slots * d.rank);
   L.part_ml = take(sizeof(float2) * slots);
   L.total = o;

@@ -7,11 +7,14 @@
 // Scores are kept in log2 units (scale * log2 e folded into one factor).  Three
 // kernels share the work split of cache_sched.cuh:
 //   rows    blocks of 64 pairs x tiles of 64 events, 4 x 4 scores and 4 x r/16 results
-//           of a thread in registers, two fp32 lanes an instruction; bound by the FMA
-//           pipe and the shared-memory reads that feed it
+//           of a thread in registers, two fp32 lanes an instruction; bound by the
+//           shared-memory reads that feed the FMA pipe (32 users, 100 to 300 new of
+//           500 to 1000 events, 4 heads: 28 TFLOP/s at r = 128, 24 at r = 64; 21 and
+//           19 with one CTA an SM and two buffers for its tiles)
 //   tokens  blocks of 8 pairs; a warp takes every 32 events by itself (a lane owns an
 //           event for the scores and columns for the result), and the warps meet at
-//           the end; bound by reading the cache
+//           the end; bound by latency at small sizes (64 users behind a window of 256,
+//           2 heads, r = 32: 14 us, of which the cache's 2 MB are 0.3)
 //   mass    tiles of 64 events against all blocks of 64 pairs; a thread sums its events
 #include <algorithm>
 
@@ -131,16 +134,19 @@ __device__ __forceinline__ void clear_rows(T* k, int n, int r, int tid, int thre
 }
 
 // ---------------------------------------------------------------- rows
+// Two CTAs an SM hide each other's loads and barriers where shared memory has the room
+// (r <= 128); at r = 256 one CTA has two buffers for its tiles.
 template <typename T, int RC>
-__global__ void __launch_bounds__(256) cache_rows_kernel(CacheAttn p) {
+__global__ void __launch_bounds__(256, RC <= 2 ? 2 : 1) cache_rows_kernel(CacheAttn p) {
+  constexpr int BUFS = RC <= 2 ? 1 : 2;
   using Line = ByRows<MT, KT>;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ CacheSplit split;
   const CacheCall& c = p.c;
   const int r = c.r, pitch = row_pitch<T>(r), tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
   T* sQ = (T*)smem;
-  T* sK = sQ + MT * pitch;                 // [2][KT][pitch]
-  float* sP = (float*)(sK + 2 * KT * pitch);   // [MT][KT + 4]
+  T* sK = sQ + MT * pitch;                 // [BUFS][KT][pitch]
+  float* sP = (float*)(sK + BUFS * KT * pitch);   // [MT][KT + 4]
   constexpr int PP = KT + 4;
   cache_split<Line>(c, p.min_quota, p.never_cut, *(CacheSplitSpace*)smem, &split);
   const CacheSplit run = split;
@@ -174,7 +180,7 @@ __global__ void __launch_bounds__(256) cache_rows_kernel(CacheAttn p) {
     };
     __syncthreads();                       // the last item's reads are done
     copy_rows(sQ, q, MT, r, tid, 256, [&](int row) { return row < rows ? q + row * r : nullptr; });
-    fetch(it.t0, 0);
+    if (BUFS == 2) fetch(it.t0, 0);
     int32_t pos[4], low[4];
     float m[4], l[4];
     bool poison[4];
@@ -191,9 +197,10 @@ __global__ void __launch_bounds__(256) cache_rows_kernel(CacheAttn p) {
       for (int k = 0; k < RC * 2; ++k) o[i][k] = make_float2(0.f, 0.f);
     }
     for (int i = it.t0; i < it.t1; ++i) {
-      const int buf = (i - it.t0) & 1;
+      const int buf = (i - it.t0) % BUFS;
       T* k = sK + buf * KT * pitch;
-      if (i + 1 < it.t1) {
+      if (BUFS == 1) fetch(i, 0);
+      if (BUFS == 2 && i + 1 < it.t1) {
         fetch(i + 1, buf ^ 1);
         copy_wait<1>();
       } else {
@@ -547,7 +554,7 @@ __global__ void __launch_bounds__(256) cache_simt_join_kernel(CacheAttn p, int m
 
 // ---------------------------------------------------------------- mass
 template <typename T>
-__global__ void __launch_bounds__(256) cache_mass_rows_kernel(CacheAttn p) {
+__global__ void __launch_bounds__(256, 2) cache_mass_rows_kernel(CacheAttn p) {
   using Line = ByTiles<MT, KT>;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ CacheSplit split;
@@ -658,7 +665,7 @@ template <typename T>
 cudaError_t attn_t(CacheAttn a, int num_sms, cudaStream_t s) {
   const int r = a.c.r, pitch = r + 16 / (int)sizeof(T);
   a.min_quota = 1;
-  int mt;
+  int mt, grid = num_sms;
   cudaError_t e;
   if (a.pairs <= TP * (int64_t)a.c.B) {
     mt = TP;
@@ -675,23 +682,25 @@ cudaError_t attn_t(CacheAttn a, int num_sms, cudaStream_t s) {
     else e = launch_with(cache_tokens_kernel<T, 8>, num_sms, 32 * warps, smem, a, s);
   } else {
     mt = MT;
-    const size_t smem = (MT + 2 * KT) * pitch * sizeof(T) + MT * (KT + 4) * 4;
+    const size_t smem = (MT + (r <= 128 ? 1 : 2) * KT) * pitch * sizeof(T) + MT * (KT + 4) * 4;
     a.never_cut = cache_most_tiles(a.c, MT, KT) <= 4;
-    if (r <= 64) e = launch_with(cache_rows_kernel<T, 1>, num_sms, 256, smem, a, s);
-    else if (r <= 128) e = launch_with(cache_rows_kernel<T, 2>, num_sms, 256, smem, a, s);
-    else e = launch_with(cache_rows_kernel<T, 4>, num_sms, 256, smem, a, s);
+    if (r <= 128) grid = 2 * num_sms;
+    if (r <= 64) e = launch_with(cache_rows_kernel<T, 1>, grid, 256, smem, a, s);
+    else if (r <= 128) e = launch_with(cache_rows_kernel<T, 2>, grid, 256, smem, a, s);
+    else e = launch_with(cache_rows_kernel<T, 4>, grid, 256, smem, a, s);
   }
   if (e != cudaSuccess || a.never_cut) return e;
-  cache_simt_join_kernel<T><<<dim3(num_sms, mt / 8), 256, 0, s>>>(a, mt);
+  cache_simt_join_kernel<T><<<dim3(grid, mt / 8), 256, 0, s>>>(a, mt);
   return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t mass_t(const CacheAttn& a, int num_sms, cudaStream_t s) {
   const size_t smem = (MT + KT) * (a.c.r + 16 / sizeof(T)) * sizeof(T);
-  cudaError_t e = launch_with(cache_mass_rows_kernel<T>, num_sms, 256, smem, a, s);
+  const int grid = a.c.r <= 128 ? 2 * num_sms : num_sms;
+  cudaError_t e = launch_with(cache_mass_rows_kernel<T>, grid, 256, smem, a, s);
   if (e != cudaSuccess) return e;
-  cache_mass_rows_join_kernel<<<num_sms, KT, 0, s>>>(a);
+  cache_mass_rows_join_kernel<<<grid, KT, 0, s>>>(a);
   return cudaGetLastError();
 }
 
