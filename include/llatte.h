@@ -544,7 +544,7 @@ int llatte_cache_append(llatte_cache* cache, const llatte_cache_view* view, cons
  * not see has no effect on it, whatever its bits; the result of a row that sees a
  * latent with an infinity or NaN is not specified (NaN where the softmax is).
  * Latents up to 2^70 in magnitude are in range.
- *   q, out       device [rows, heads, rank] in dtype, 16-byte aligned; rows of
+ *   q, out       device [rows, heads, rank] in dtype, 16-byte aligned, apart; rows of
  *                `out` that belong to no user are left as they were
  *   lse          device fp32 [rows, heads], or NULL
  *   window       events a row sees back from its position, itself included

@@ -626,8 +626,9 @@ int cache_layer_check(const llatte_cache* h, const llatte_cache_view* v, int hea
 }
 
 int cache_layer_run(llatte_cache* h, const llatte_cache_view* v, const CacheLayer& l,
-                    cudaStream_t s) {
+                    int* launched, cudaStream_t s) {
   if (l.rows_h > 0) {
+    ++*launched;
     CacheAppend ap = {};
     ap.c = make_call(h, v, l.hoff, l.rows_h);
     ap.pool = h->pool; ap.mass = h->mass; ap.x = l.C;
@@ -638,6 +639,7 @@ int cache_layer_run(llatte_cache* h, const llatte_cache_view* v, const CacheLaye
   a.lse2 = l.accumulate ? h->lse2 : nullptr;
   a.scale2 = l.scale2;
   a.pairs = l.pairs;
+  a.launched = launched;
   return run_attn(h, a, s) == cudaSuccess ? LLATTE_OK : LLATTE_ERR_CUDA;
 }
 
@@ -738,7 +740,7 @@ int llatte_cache_attend(llatte_cache* h, const llatte_cache_view* v, const llatt
     return LLATTE_ERR_ARG;
   if (p->accumulate && !h->mass) return LLATTE_ERR_ARG;
   if (v->B == 0 || p->rows == 0) return LLATTE_OK;
-  if (!p->q || !p->out || !p->q_offsets || (((uintptr_t)p->q | (uintptr_t)p->out) & 15))
+  if (!p->q || !p->out || p->q == p->out || !p->q_offsets || (((uintptr_t)p->q | (uintptr_t)p->out) & 15))
     return LLATTE_ERR_ARG;
   DeviceGuard g(h->device);
   if (!g.ok) return LLATTE_ERR_CUDA;

@@ -46,6 +46,7 @@ struct CacheAttn {
   float2* part_ml;           // [2 CTAs, block rows] maximum (log2 units) and sum
   CacheJoin* join;           // [CTAs]
   int32_t* count;            // [CTAs] parts done of the block that begins there; 0 between calls
+  int* launched;             // host: kernels launched are added here (or NULL)
   int64_t pairs;             // (row, head) pairs of the call, as far as the host can tell
   int32_t min_quota;         // fewest tiles of a CTA's run
   bool never_cut;            // no block is cut between CTAs (then there is nothing to join)
@@ -65,7 +66,7 @@ struct CacheLayer {
 int cache_layer_check(const llatte_cache* h, const llatte_cache_view* v, int heads, int rank,
                       int dtype, int64_t rows_q, int accumulate);
 int cache_layer_run(llatte_cache* h, const llatte_cache_view* v, const CacheLayer& a,
-                    cudaStream_t s);
+                    int* launched, cudaStream_t s);
 
 struct CacheAppend {
   CacheCall c;
@@ -96,6 +97,10 @@ inline int64_t cache_most_tiles(const CacheCall& c, int mt, int kt) {
   const int64_t span = (int64_t)c.window + mt / c.heads;       // of the windows of its rows
   const int64_t w = (span + kt - 1) / kt + 1 + ((int64_t)c.n_sink + kt - 1) / kt;
   return t < w ? t : w;
+}
+
+inline void cache_launched(const CacheAttn& a, int n) {
+  if (a.launched) *a.launched += n;
 }
 
 cudaError_t launch_cache_append(int elem, const CacheAppend& a, cudaStream_t s);

@@ -809,6 +809,7 @@ cudaError_t launch_r(CacheAttn a, const CUtensorMap& tmC, int num_sms, cudaStrea
     return cudaErrorInvalidValue;
   const cudaError_t e = launch_dependent(cache_attn_kernel<R>, dim3(num_sms), dim3(kThreads), C::SMEM,
                                          s, 1, tmQ, tmC, tmO, a);
+  cache_launched(a, a.never_cut ? 1 : 2);
   if (e != cudaSuccess || a.never_cut) return e;
   return launch_dependent(cache_join_kernel<R>, dim3(num_sms, MT / 8), dim3(256), 0, s, 1, a);
 }

@@ -357,6 +357,7 @@ cudaError_t launch_rn(const CacheAttn& a, const CUtensorMap& tmC, int num_sms, c
   CUtensorMap tmQ;
   if (!make_tmap_bf16(&tmQ, a.q, (uint64_t)a.c.rows * a.c.heads, R, NP))
     return cudaErrorInvalidValue;
+  cache_launched(a, 2);
   cudaError_t e = launch_dependent(cache_mass_kernel<R>, dim3(num_sms), dim3(kThreads),
                                    C::SMEM, s, 1, tmQ, tmC, a);
   if (e != cudaSuccess) return e;

@@ -689,6 +689,7 @@ cudaError_t attn_t(CacheAttn a, int num_sms, cudaStream_t s) {
     else if (r <= 128) e = launch_with(cache_rows_kernel<T, 2>, grid, 256, smem, a, s);
     else e = launch_with(cache_rows_kernel<T, 4>, grid, 256, smem, a, s);
   }
+  cache_launched(a, a.never_cut ? 1 : 2);
   if (e != cudaSuccess || a.never_cut) return e;
   cache_simt_join_kernel<T><<<dim3(grid, mt / 8), 256, 0, s>>>(a, mt);
   return cudaGetLastError();
@@ -700,6 +701,7 @@ cudaError_t mass_t(const CacheAttn& a, int num_sms, cudaStream_t s) {
   const int grid = a.c.r <= 128 ? 2 * num_sms : num_sms;
   cudaError_t e = launch_with(cache_mass_rows_kernel<T>, grid, 256, smem, a, s);
   if (e != cudaSuccess) return e;
+  cache_launched(a, 2);
   cache_mass_rows_join_kernel<<<grid, KT, 0, s>>>(a);
   return cudaGetLastError();
 }

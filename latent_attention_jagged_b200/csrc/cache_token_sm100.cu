@@ -636,6 +636,7 @@ cudaError_t launch_mass_r(const CacheAttn& a, const CUtensorMap& tmC, int num_sm
     if (e != cudaSuccess) return e;
     attr_devices |= 1ull << (dev & 63);
   }
+  cache_launched(a, 1);
   return launch_dependent(cache_mass_token_kernel<R>, dim3(num_sms), dim3(kThreads), C::SMEM, s, 1,
                           tmC, a);
 }
@@ -657,6 +658,7 @@ cudaError_t launch_r(CacheAttn a, const CUtensorMap& tmC, int num_sms, cudaStrea
     if (f.numRegs * 3 < 2 * kRegsConsume + kRegsProduce) return cudaErrorInvalidConfiguration;
     attr_devices |= 1ull << (dev & 63);
   }
+  cache_launched(a, 1);
   return launch_dependent(cache_token_kernel<R>, dim3(num_sms), dim3(kThreads), C::SMEM, s, 1, tmC,
                           a);
 }

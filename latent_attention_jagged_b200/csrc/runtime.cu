@@ -860,9 +860,10 @@ int forward_impl(llatte_handle* h, const void* values, const int64_t* offsets, i
       a.n_cand = D.n_q; a.window = fc->window; a.n_sink = fc->n_sink;
       a.accumulate = fc->accumulate;
       a.scale2 = tc ? 1.f : 1.4426950408889634f;   // log2 e is folded into the tensor-core q~
-      const int rc = cache_layer_run(fc->caches[l], &fc->views[l], a, s);
+      int launched = 0;
+      const int rc = cache_layer_run(fc->caches[l], &fc->views[l], a, &launched, s);
       if (rc != LLATTE_OK) return rc;
-      t.done(fc->accumulate ? 5 : 3);
+      t.done(launched);
     } else if (tc) {  // latent attention, tensor cores
       StepTimer t(h, s, ST_ATTN);
       AttnTcParams a = {};

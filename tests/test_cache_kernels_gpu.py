@@ -9,8 +9,8 @@ import torch
 
 import oracle.cache as oc
 from cache_harness import DT, Case, attend_bounds, check_attend, close, mass_bound
-from latent_attention_jagged_b200 import LatentCache
-from latent_attention_jagged_b200.binding import DEV_BAD_ID
+from latent_attention_jagged_b200 import LatentCache, LlatteError
+from latent_attention_jagged_b200.binding import DEV_BAD_ID, LLATTE_ERR_ARG
 
 pytestmark = pytest.mark.gpu
 
@@ -201,5 +201,13 @@ def test_a_closed_cache_refuses():
     q, off = c.queries([1], 0)
     extra = LatentCache(c.pool, 4, max_batch=1, max_rows=4, max_pages=2)
     extra.close()
-    with pytest.raises(Exception):
+    with pytest.raises(LlatteError):
         extra.attend(q, torch.from_numpy(off).cuda(), c.dev("table"), c.dev("lengths"))
+
+
+def test_the_result_may_not_replace_the_queries():
+    c = Case("bf16", 4, 128, 64, [70], seed=63)
+    q, off = c.queries([1], 0)
+    with pytest.raises(LlatteError) as e:
+        c.cache.attend(q, torch.from_numpy(off).cuda(), c.dev("table"), c.dev("lengths"), out=q)
+    assert e.value.code == LLATTE_ERR_ARG
