@@ -179,6 +179,47 @@ __device__ __forceinline__ int block_scan(int v, int* warps, int* all) {
   return before + incl - v;
 }
 
+// Moves n kept rows of user u to other pages: a warp copies whole rows, 4 at a time, in
+// turns of kCopyRows.  Bound by HBM where there are many users: 134 MB in 26 us (256
+// users, 512 rows of 512 bytes).
+constexpr int kCopyRows = 16;
+__device__ __forceinline__ void copy_kept(const CacheEvict& a, int u, int n, int warp, int warps,
+                                          int nvec) {
+  const CacheCall& c = a.c;
+  const int lane = threadIdx.x & 31;
+  const int32_t* list = a.list + (int64_t)u * a.list_stride;
+#pragma unroll 1
+  for (int i0 = warp * kCopyRows; i0 < n; i0 += warps * kCopyRows) {
+    // lane l: place of row i0 + l
+    int64_t src = -1, dst = -1;
+    if (lane < kCopyRows && i0 + lane < n) {
+      src = cache_row(c, c.table, c.stride, u, list[i0 + lane]);
+      dst = cache_row(c, a.dst_table, a.dst_stride, u, i0 + lane);
+      if (dst >= 0) a.mass[dst] = src < 0 ? 0.f : a.mass[src];
+    }
+    const int rows = min(kCopyRows, n - i0);
+    for (int r = 0; r < rows; r += 4) {
+      int64_t s[4], d[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        s[k] = __shfl_sync(0xffffffffu, src, r + k);
+        d[k] = __shfl_sync(0xffffffffu, dst, r + k);
+      }
+      for (int col = lane; col < nvec; col += 32) {
+        uint4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          v[k] = make_uint4(0, 0, 0, 0);
+          if (s[k] >= 0) v[k] = __ldcs((const uint4*)a.pool + s[k] * nvec + col);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (d[k] >= 0) ((uint4*)a.pool)[d[k] * nvec + col] = v[k];
+      }
+    }
+  }
+}
+
 // Users of up to NK * kSelThreads events: the keys are read once and stay in
 // registers, NK neighbours a thread.  The threshold, the need-th largest key of the
 // events that do not stay anyway, is found bit by bit from the highest bit in which
@@ -186,14 +227,21 @@ __device__ __forceinline__ int block_scan(int v, int* warps, int* all) {
 // block place the kept slots in order, events at the threshold going to the earliest
 // slots.  (Digits with histograms in shared memory took 31 us for 256 users of 700 to
 // 1600 events: heavy-tailed masses fall into a few bins.)
+// With copy_nvec > 0 the block then moves the rows as well.
 template <int NK>
-__global__ void __launch_bounds__(kSelThreads) cache_select_kernel(CacheEvict a) {
+__global__ void __launch_bounds__(kSelThreads) cache_select_kernel(CacheEvict a, int copy_nvec) {
   __shared__ int s_warp[2][kSelThreads / 32];
   const CacheCall& c = a.c;
   const int u = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   CacheUser x;
   tc::pdl_trigger();
-  if (!select_start(a, u, &x)) return;
+  const bool chosen = !select_start(a, u, &x);
+  if (chosen && copy_nvec == 0) return;
+  if (chosen) {                         // a user that keeps all its events, or none
+    __syncthreads();
+    copy_kept(a, u, a.count[u], warp, kSelThreads / 32, copy_nvec);
+    return;
+  }
   const int T = x.len, K = a.budget, lo = c.n_sink, hi = T - a.n_recent;   // [lo, hi): may go
   const int need = K - c.n_sink - a.n_recent;
   const int t0 = threadIdx.x * NK;
@@ -272,6 +320,9 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(CacheEvict a)
       if (kept) kept[at] = t0 + i;
       ++at;
     }
+  if (copy_nvec == 0) return;
+  __syncthreads();                      // the list is read by other threads
+  copy_kept(a, u, min(T, K), warp, kSelThreads / 32, copy_nvec);
 }
 
 // Longer users: the threshold is found digit by digit (8 bits, from the top) with a
@@ -403,46 +454,11 @@ cache_move_kernel(CacheEvict a, int row_bytes, int slices) {
   }
 }
 
-// Moves the kept rows to other pages: a warp copies whole rows, 4 at a time.  Bound by
-// HBM: 134 MB in 26 us (256 users, 512 rows of 512 bytes).
-constexpr int kCopyRows = 16;              // rows of a warp's turn
 __global__ void __launch_bounds__(kMoveThreads)
 cache_copy_kernel(CacheEvict a, int nvec) {
   tc::pdl_wait();
-  const CacheCall& c = a.c;
-  const int u = blockIdx.y, lane = threadIdx.x & 31;
-  const int n = a.count[u];
-  const int32_t* list = a.list + (int64_t)u * a.list_stride;
-  for (int i0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * kCopyRows; i0 < n;
-       i0 += gridDim.x * 8 * kCopyRows) {
-    // lane l: place of row i0 + l
-    int64_t src = -1, dst = -1;
-    if (lane < kCopyRows && i0 + lane < n) {
-      src = cache_row(c, c.table, c.stride, u, list[i0 + lane]);
-      dst = cache_row(c, a.dst_table, a.dst_stride, u, i0 + lane);
-      if (dst >= 0) a.mass[dst] = src < 0 ? 0.f : a.mass[src];
-    }
-    const int rows = min(kCopyRows, n - i0);
-    for (int r = 0; r < rows; r += 4) {
-      int64_t s[4], d[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        s[k] = __shfl_sync(0xffffffffu, src, r + k);
-        d[k] = __shfl_sync(0xffffffffu, dst, r + k);
-      }
-      for (int col = lane; col < nvec; col += 32) {
-        uint4 v[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          v[k] = make_uint4(0, 0, 0, 0);
-          if (s[k] >= 0) v[k] = __ldcs((const uint4*)a.pool + s[k] * nvec + col);
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (d[k] >= 0) ((uint4*)a.pool)[d[k] * nvec + col] = v[k];
-      }
-    }
-  }
+  copy_kept(a, blockIdx.y, a.count[blockIdx.y], blockIdx.x * 8 + (threadIdx.x >> 5), gridDim.x * 8,
+            nvec);
 }
 
 template <typename T, int G, int NV, int STEPS>
@@ -482,11 +498,20 @@ cudaError_t launch_cache_append(int elem, const CacheAppend& a, cudaStream_t s) 
 
 cudaError_t launch_cache_evict(int elem, const CacheEvict& a, cudaStream_t s) {
   const int64_t most = std::min<int64_t>(a.c.cap, a.budget);    // kept events of a user
-  if (a.c.cap <= 4 * kSelThreads) cache_select_kernel<4><<<a.c.B, kSelThreads, 0, s>>>(a);
-  else if (a.c.cap <= 16 * kSelThreads) cache_select_kernel<16><<<a.c.B, kSelThreads, 0, s>>>(a);
-  else cache_select_long_kernel<<<a.c.B, kSelThreads, 0, s>>>(a);
   const int row_bytes = a.c.r * elem;
-  if (a.dst_table != a.c.table) {
+  const bool apart = a.dst_table != a.c.table;
+  // To other pages the selecting block moves its user's rows itself where they are few,
+  // or where the users fill the GPU (256 users, 512 rows of 512 bytes: 35 us, 40 with a
+  // second launch; 4 users, 128 rows of 128 bytes: 12.3 and 13.6); a launch that spreads
+  // a user's rows over the GPU does it otherwise.
+  const bool fused = apart && a.c.cap <= 16 * kSelThreads &&
+                     (most * row_bytes <= 64 * 1024 || a.c.B >= 128);
+  const int nvec = fused ? row_bytes / 16 : 0;
+  if (a.c.cap <= 4 * kSelThreads) cache_select_kernel<4><<<a.c.B, kSelThreads, 0, s>>>(a, nvec);
+  else if (a.c.cap <= 16 * kSelThreads) cache_select_kernel<16><<<a.c.B, kSelThreads, 0, s>>>(a, nvec);
+  else cache_select_long_kernel<<<a.c.B, kSelThreads, 0, s>>>(a);
+  if (fused) return cudaGetLastError();
+  if (apart) {
     const int blocks = (int)std::min<int64_t>((most + 8 * kCopyRows - 1) / (8 * kCopyRows), 64);
     return tc::launch_dependent(cache_copy_kernel, dim3(blocks, a.c.B), dim3(kMoveThreads), 0, s, 1,
                                 a, row_bytes / 16);
