@@ -46,6 +46,8 @@ template <typename T, int G, int NV, int STEPS>
 __global__ void __launch_bounds__(256) cache_append_kernel(CacheAppend a) {
   constexpr int EV = 16 / sizeof(T), STEP = 32 / G, ROWS = STEPS * STEP;
   static_assert(ROWS <= 32, "one lane finds the place of a row");
+  tc::pdl_trigger();
+  tc::pdl_wait();
   const CacheCall& c = a.c;
   const int lane = threadIdx.x & 31;
   const int64_t row0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * ROWS;
@@ -235,6 +237,7 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(CacheEvict a,
   const int u = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   CacheUser x;
   tc::pdl_trigger();
+  tc::pdl_wait();
   const bool chosen = !select_start(a, u, &x);
   if (chosen && copy_nvec == 0) return;
   if (chosen) {                         // a user that keeps all its events, or none
@@ -329,6 +332,8 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(CacheEvict a,
 // histogram of the keys that share the digits found so far, reading the masses again
 // for every digit; then one pass in slot order writes the kept slots.
 __global__ void __launch_bounds__(kSelThreads) cache_select_long_kernel(CacheEvict a) {
+  tc::pdl_trigger();
+  tc::pdl_wait();
   __shared__ int hist[256];
   __shared__ uint32_t s_prefix;
   __shared__ int s_need;
@@ -464,9 +469,8 @@ cache_copy_kernel(CacheEvict a, int nvec) {
 template <typename T, int G, int NV, int STEPS>
 cudaError_t append_s(const CacheAppend& a, cudaStream_t s) {
   constexpr int rows = 8 * STEPS * 32 / G;
-  cache_append_kernel<T, G, NV, STEPS>
-      <<<(unsigned)((a.c.rows + rows - 1) / rows), 256, 0, s>>>(a);
-  return cudaGetLastError();
+  return tc::launch_dependent(cache_append_kernel<T, G, NV, STEPS>,
+                              dim3((unsigned)((a.c.rows + rows - 1) / rows)), dim3(256), 0, s, 1, a);
 }
 
 // A block lives as long as its chain of loads, whatever it moves: with more rows than one
@@ -507,10 +511,14 @@ cudaError_t launch_cache_evict(int elem, const CacheEvict& a, cudaStream_t s) {
   const bool fused = apart && a.c.cap <= 16 * kSelThreads &&
                      (most * row_bytes <= 64 * 1024 || a.c.B >= 128);
   const int nvec = fused ? row_bytes / 16 : 0;
-  if (a.c.cap <= 4 * kSelThreads) cache_select_kernel<4><<<a.c.B, kSelThreads, 0, s>>>(a, nvec);
-  else if (a.c.cap <= 16 * kSelThreads) cache_select_kernel<16><<<a.c.B, kSelThreads, 0, s>>>(a, nvec);
-  else cache_select_long_kernel<<<a.c.B, kSelThreads, 0, s>>>(a);
-  if (fused) return cudaGetLastError();
+  const dim3 users(a.c.B), threads(kSelThreads);
+  const cudaError_t e =
+      a.c.cap <= 4 * kSelThreads
+          ? tc::launch_dependent(cache_select_kernel<4>, users, threads, 0, s, 1, a, nvec)
+      : a.c.cap <= 16 * kSelThreads
+          ? tc::launch_dependent(cache_select_kernel<16>, users, threads, 0, s, 1, a, nvec)
+          : tc::launch_dependent(cache_select_long_kernel, users, threads, 0, s, 1, a);
+  if (e != cudaSuccess || fused) return e;
   if (apart) {
     const int blocks = (int)std::min<int64_t>((most + 8 * kCopyRows - 1) / (8 * kCopyRows), 64);
     return tc::launch_dependent(cache_copy_kernel, dim3(blocks, a.c.B), dim3(kMoveThreads), 0, s, 1,

@@ -148,6 +148,8 @@ __global__ void __launch_bounds__(256, RC <= 2 ? 2 : 1) cache_rows_kernel(CacheA
   T* sK = sQ + MT * pitch;                 // [BUFS][KT][pitch]
   float* sP = (float*)(sK + BUFS * KT * pitch);   // [MT][KT + 4]
   constexpr int PP = KT + 4;
+  tc::pdl_trigger();
+  tc::pdl_wait();
   cache_split<Line>(c, p.min_quota, p.never_cut, *(CacheSplitSpace*)smem, &split);
   const CacheSplit run = split;
   CacheJoin* join = p.join + blockIdx.x;
@@ -331,6 +333,8 @@ __global__ void __launch_bounds__(256) cache_tokens_kernel(CacheAttn p) {
   float* sW = sQ + TP * r + warp * TP * TK;
   T* sK = (T*)(sQ + TP * r + warps * TP * TK) + warp * 2 * TK * pitch;
   float* sO = sQ + TP * r + warps * TP * TK;
+  tc::pdl_trigger();
+  tc::pdl_wait();
   cache_split<Line>(c, p.min_quota, p.never_cut, *(CacheSplitSpace*)smem, &split);
   const CacheSplit run = split;
   CacheJoin* join = p.join + blockIdx.x;
@@ -523,6 +527,8 @@ __global__ void __launch_bounds__(256) cache_tokens_kernel(CacheAttn p) {
 // the events.  One warp per row.
 template <typename T>
 __global__ void __launch_bounds__(256) cache_simt_join_kernel(CacheAttn p, int mt) {
+  tc::pdl_trigger();
+  tc::pdl_wait();
   const CacheJoin j = p.join[blockIdx.x];
   const int lane = threadIdx.x & 31, r = p.c.r;
   const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
@@ -565,6 +571,8 @@ __global__ void __launch_bounds__(256, 2) cache_mass_rows_kernel(CacheAttn p) {
   const int r = c.r, pitch = row_pitch<T>(r), tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
   T* sK = (T*)smem;
   T* sQ = sK + KT * pitch;
+  tc::pdl_trigger();
+  tc::pdl_wait();
   cache_split<Line>(c, 1, false, *(CacheSplitSpace*)smem, &split);
   const CacheSplit run = split;
   CacheJoin* join = p.join + blockIdx.x;
@@ -636,6 +644,8 @@ __global__ void __launch_bounds__(256, 2) cache_mass_rows_kernel(CacheAttn p) {
 }
 
 __global__ void __launch_bounds__(KT) cache_mass_rows_join_kernel(CacheAttn p) {
+  tc::pdl_trigger();
+  tc::pdl_wait();
   const CacheJoin j = p.join[blockIdx.x];
   if ((int)threadIdx.x >= j.rows) return;
   const CacheCall& c = p.c;
@@ -657,8 +667,7 @@ cudaError_t launch_with(K kernel, int grid, int threads, size_t smem, const Cach
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)smem);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, threads, smem, s>>>(a);
-  return cudaGetLastError();
+  return tc::launch_dependent(kernel, dim3(grid), dim3(threads), smem, s, 1, a);
 }
 
 template <typename T>
@@ -691,8 +700,8 @@ cudaError_t attn_t(CacheAttn a, int num_sms, cudaStream_t s) {
   }
   cache_launched(a, a.never_cut ? 1 : 2);
   if (e != cudaSuccess || a.never_cut) return e;
-  cache_simt_join_kernel<T><<<dim3(grid, mt / 8), 256, 0, s>>>(a, mt);
-  return cudaGetLastError();
+  return tc::launch_dependent(cache_simt_join_kernel<T>, dim3(grid, mt / 8), dim3(256), 0, s, 1, a,
+                              mt);
 }
 
 template <typename T>
@@ -702,8 +711,7 @@ cudaError_t mass_t(const CacheAttn& a, int num_sms, cudaStream_t s) {
   cudaError_t e = launch_with(cache_mass_rows_kernel<T>, grid, 256, smem, a, s);
   if (e != cudaSuccess) return e;
   cache_launched(a, 2);
-  cache_mass_rows_join_kernel<<<grid, KT, 0, s>>>(a);
-  return cudaGetLastError();
+  return tc::launch_dependent(cache_mass_rows_join_kernel, dim3(grid), dim3(KT), 0, s, 1, a);
 }
 
 }  // namespace

@@ -511,6 +511,7 @@ cache_mass_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn
   CacheItem<Line> it;
   if (warp == NW) {
     uint32_t g = 0;
+    const uint64_t policy = policy_stream(true);
     const int32_t P = min(1 << c.page_shift, kCacheBox);
     const int np = KT / P;
     const int32_t outside = c.n_pages << c.page_shift;
@@ -536,7 +537,7 @@ cache_mass_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn
         uint8_t* dst = sKV + st * C::KV_BYTES + lane * P * 128;
 #pragma unroll
         for (int s = 0; s < RSUB; ++s)
-          tma_load_2d(&tmC, &kv_full[st], dst + s * C::KV_SUB, s * 64, y);
+          tma_load_2d_hint(&tmC, &kv_full[st], dst + s * C::KV_SUB, s * 64, y, policy);
       }
       ++g;
     }
