@@ -12,6 +12,11 @@
 //
 // One item = a tile of one user and a run of the blocks of pairs that see it; a
 // tile cut between CTAs is summed from parts by a second kernel.
+//
+// What bounds it: a block is 1024 cycles of the exponentials (128 x 128, 16 a cycle) and
+// about as many issue slots; it takes about 1600, and every item begins with the walk
+// of the run and ends with a meeting of the warps (64 candidates for 256 users, r =
+// 128: 34 us, of which 5 are the beginning).
 #include <cuda.h>
 
 #include <algorithm>
@@ -33,22 +38,22 @@ namespace {
 constexpr int KT = 128;                   // events of a tile
 constexpr int NP = 128;                   // pairs of a block
 
-// Two groups of 8 warps take the blocks of pairs in turn; of a group, two warps share
-// 32 events (half of the pairs each).
+// Four softmax warps share 32 events, a quarter of a block's pairs each; a warp goes on
+// to the next block by itself.
 constexpr int kSoft0 = 2, kSoft = 16;
 constexpr int kThreads = 32 * (kSoft0 + kSoft);
 
 template <int R>
 struct Cfg {
   static constexpr int RSUB = R / 64;
-  static constexpr int CP = NP / 2;                    // pairs of a softmax warp
+  static constexpr int CP = NP / 4;                    // pairs of a softmax warp
   static constexpr int SB = 4;                         // S^T buffers in tensor memory
   static constexpr int KS = R == 256 ? 1 : 2;          // ring slots: a tile stays for many blocks
   static constexpr int QS = R == 256 ? 2 : 4;
   static constexpr uint32_t KSUB = KT * 128, K_BYTES = RSUB * KSUB;
   static constexpr uint32_t QSUB = NP * 128, Q_BYTES = RSUB * QSUB;
   static constexpr uint32_t BAR_BYTES = R == 256 ? 256 : 384;
-  static constexpr uint32_t F_BYTES = kSoft * CP * 12 + 3 * 128 * 4;   // of the pairs; sums
+  static constexpr uint32_t F_BYTES = kSoft * CP * 12 + 6 * 128 * 4;   // of the pairs; sums
   static constexpr size_t SMEM = 1024 + KS * K_BYTES + QS * Q_BYTES + BAR_BYTES + F_BYTES;
   static constexpr uint32_t TMEM_COLS = SB * NP;
   static_assert(SMEM <= 232448, "shared memory budget");
@@ -83,8 +88,8 @@ cache_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   CacheSplit* split = (CacheSplit*)(tmem_slot + 2);
   static_assert((2 * KS + 2 * QS + 2 * SB + 5) * 8 + 8 + sizeof(CacheSplit) <= C::BAR_BYTES,
                 "barriers");
-  float* sums = (float*)((uint8_t*)bars + C::BAR_BYTES);   // [3][128]
-  float* pbuf = sums + 3 * 128;                              // [kSoft][3][CP] of the pairs
+  float* sums = (float*)((uint8_t*)bars + C::BAR_BYTES);   // [2][3][128]
+  float* pbuf = sums + 6 * 128;                              // [kSoft][3][CP] of the pairs
 
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -93,7 +98,7 @@ cache_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   if (threadIdx.x == 0) {
     for (int s = 0; s < KS; ++s) { mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 1); }
     for (int s = 0; s < QS; ++s) { mbar_init(&q_full[s], 1); mbar_init(&q_empty[s], 1); }
-    for (int s = 0; s < SB; ++s) { mbar_init(&s_full[s], 1); mbar_init(&s_empty[s], kSoft / 2); }
+    for (int s = 0; s < SB; ++s) { mbar_init(&s_full[s], 1); mbar_init(&s_empty[s], kSoft); }
     for (int q = 0; q < 4; ++q) mbar_init(&pair_bar[q], 4);
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -214,8 +219,7 @@ cache_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax
-    const int quad = warp & 3, part = ((warp - kSoft0) >> 2) & 1;   // events, half of the pairs
-    const int group = (warp - kSoft0) >> 3;
+    const int quad = warp & 3, part = (warp - kSoft0) >> 2;   // events, quarter of the pairs
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
     // of this warp's pairs: log sum, last and first event inside the window
     float* lw = pbuf + (warp - kSoft0) * 3 * CP;
@@ -224,7 +228,7 @@ cache_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     CacheJoin* join = p.join + blockIdx.x;
     const bool writer = warp == kSoft0 && lane == 0;
     if (writer) join->rows = 0;
-    uint32_t qn = 0, done = 0, pphase = 0;   // blocks, and those before this piece
+    uint32_t qn = 0, pphase = 0;
     bool ok = true;
     CacheItems<Line> items;
     items.start(c, run);
@@ -236,79 +240,64 @@ cache_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       const uint32_t pairs = (uint32_t)it.x.n * (uint32_t)c.heads;
       // the first events are inside every window
       const int32_t tw = t < c.n_sink ? INT32_MAX : t;
-      // log sums of this lane's two pairs of block i
+      // this lane's pair of block i, and its log sum
       const float* lse = p.lse2 + it.x.row0 * c.heads;
-      auto pair_of = [&](int i, int k) -> uint32_t {
-        return (uint32_t)(it.k.first + i) * NP + part * CP + lane + 32 * k;
-      };
-      auto ask = [&](int i, float (&v)[2]) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) v[k] = i < it.t1 && pair_of(i, k) < pairs ? lse[pair_of(i, k)] : 0.f;
-      };
-      float sum = 0.f, next[2];
-      const int i0 = it.t0 + (int)((qn ^ group) & 1);      // this group's first block
-      qn += i0 - it.t0;
-      ask(i0, next);
-      for (int i = i0; i < it.t1; i += 2, qn += 2) {
+      auto pair_of = [&](int i) { return (uint32_t)(it.k.first + i) * NP + part * CP + lane; };
+      auto ask = [&](int i) { return i < it.t1 && pair_of(i) < pairs ? lse[pair_of(i)] : 0.f; };
+      // where the first quarter puts the sums
+      int64_t at = -1;
+      if (part == 0 && it.whole && t <= all.pmax &&
+          (t >= cache_low(c, all.pmin) || t < c.n_sink))
+        at = cache_row(c, c.table, c.stride, it.u, t);
+      float sum = 0.f, next = ask(it.t0);
+      for (int i = it.t0; i < it.t1; ++i, ++qn) {
         const int sb = qn % SB;
         __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t pair = pair_of(i, k);
-          const int32_t pos = pair < pairs ? cache_pos(it.x, cache_div(c, pair)) : -1;
-          lw[lane + 32 * k] = next[k];
-          pw[lane + 32 * k] = pos;
-          ww[lane + 32 * k] = cache_low(c, pos);
-        }
-        ask(i + 2, next);                  // on its way while this block is summed
+        const int32_t pos = pair_of(i) < pairs ? cache_pos(it.x, cache_div(c, pair_of(i))) : -1;
+        lw[lane] = next;
+        pw[lane] = pos;
+        ww[lane] = cache_low(c, pos);
+        next = ask(i + 1);                 // on its way while this block is summed
         __syncwarp();
         bool w = mbar_wait(&s_full[sb], (qn / SB) & 1, abort_flag, c.status);
         if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
         tc_fence_after();
         float s4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-        for (int h = 0; h < CP; h += 32) {
-          float v[32];
-          tmem_ld32(lane_base + sb * NP + part * CP + h, v);
-          if (h + 32 == CP) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s_empty[sb]);
-          }
+        float v[CP];
+        static_assert(CP == 32, "columns of a load");
+        tmem_ld32(lane_base + sb * NP + part * CP, v);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_empty[sb]);
 #pragma unroll
-          for (int k = 0; k < 32; k += 4) {
-            const float4 l4 = *(const float4*)(lw + h + k);
-            const int4 p4 = *(const int4*)(pw + h + k), w4 = *(const int4*)(ww + h + k);
-            const float e0 = ex2_approx(fmaf(v[k], p.scale2, -l4.x));
-            const float e1 = ex2_approx(fmaf(v[k + 1], p.scale2, -l4.y));
-            const float e2 = ex2_approx(fmaf(v[k + 2], p.scale2, -l4.z));
-            const float e3 = ex2_approx(fmaf(v[k + 3], p.scale2, -l4.w));
-            if (t <= p4.x && tw >= w4.x) s4[0] += e0;
-            if (t <= p4.y && tw >= w4.y) s4[1] += e1;
-            if (t <= p4.z && tw >= w4.z) s4[2] += e2;
-            if (t <= p4.w && tw >= w4.w) s4[3] += e3;
-          }
+        for (int k = 0; k < CP; k += 4) {
+          const float4 l4 = *(const float4*)(lw + k);
+          const int4 p4 = *(const int4*)(pw + k), w4 = *(const int4*)(ww + k);
+          const float e0 = ex2_approx(fmaf(v[k], p.scale2, -l4.x));
+          const float e1 = ex2_approx(fmaf(v[k + 1], p.scale2, -l4.y));
+          const float e2 = ex2_approx(fmaf(v[k + 2], p.scale2, -l4.z));
+          const float e3 = ex2_approx(fmaf(v[k + 3], p.scale2, -l4.w));
+          if (t <= p4.x && tw >= w4.x) s4[0] += e0;
+          if (t <= p4.y && tw >= w4.y) s4[1] += e1;
+          if (t <= p4.z && tw >= w4.z) s4[2] += e2;
+          if (t <= p4.w && tw >= w4.w) s4[3] += e3;
         }
         sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
       }
       if (!ok) break;
-      qn = done + (uint32_t)(it.t1 - it.t0);
-      done = qn;
-      // the groups' halves of the pairs meet, in this order
-      const int lead = group * 2 + part;
-      if (lead) sums[(lead - 1) * 128 + quad * 32 + lane] = sum;
+      // the quarters of the pairs meet, in this order (two sets of sums: the next
+      // piece's are written while these are read)
+      float* meet = sums + (pphase & 1) * 3 * 128;
+      if (part) meet[(part - 1) * 128 + quad * 32 + lane] = sum;
       if (!group_sync(&pair_bar[quad], pphase, abort_flag, c.status)) break;
-      if (lead == 0) {
+      if (part == 0) {
 #pragma unroll
-        for (int k = 0; k < 3; ++k) sum += sums[k * 128 + quad * 32 + lane];
-        if (!it.whole) {
+        for (int k = 0; k < 3; ++k) sum += meet[k * 128 + quad * 32 + lane];
+        if (!it.whole)
           p.part_ml[((int64_t)blockIdx.x * 2 + (it.starts ? 1 : 0)) * KT + quad * 32 + lane].x = sum;
-        } else if (t <= all.pmax && (t >= cache_low(c, all.pmin) || t < c.n_sink)) {
-          const int64_t at = cache_row(c, c.table, c.stride, it.u, t);
-          if (at >= 0) atomicAdd(&p.mass[at], sum);
-        }
+        else if (at >= 0)
+          atomicAdd(&p.mass[at], sum);
       }
-      if (!group_sync(&pair_bar[quad], pphase, abort_flag, c.status)) break;
       if (writer && !it.whole && it.starts) {
         join->pair0 = ((int64_t)it.u << 32) | (uint32_t)tile0;
         join->parts = it.parts;
