@@ -599,10 +599,13 @@ int llatte_cache_evict(llatte_cache* cache, const llatte_cache_view* view,
 /*
  * A forward pass over cached histories: `batch` holds only the new events of
  * every user (and the query tokens), and each layer appends its latents of them
- * to its cache and attends over that.  For a model whose layers keep every row
- * (keep[l] >= max_len in every layer) the result is llatte_forward's on the whole
- * histories; after eviction, or with a window, it is the attention over what is
- * left.  The context must be the one the cached events were computed with.
+ * to its cache and attends over that.  Every layer must keep every cached event: with
+ * K = the smallest keep[l], max_len (which bounds the new events here) may not exceed K,
+ * no layer's pages may hold more than K events (rounded up to whole pages), and a
+ * user whose length exceeds K is left out (LLATTE_DEV_TOO_LONG).  The result is then
+ * llatte_forward's on the whole histories; after eviction, or with a window, it is the
+ * attention over what is left.  The context must be the one the cached events were
+ * computed with.
  *   caches      host array [n_layers], one cache per layer, of the handle's heads,
  *               rank and dtype, with max_rows >= the handle's query rows
  *               (min(max_total or max_batch * max_len, max_batch * keep[0])
@@ -613,7 +616,8 @@ int llatte_cache_evict(llatte_cache* cache, const llatte_cache_view* view,
  * LLATTE_ERR_UNSUPPORTED for a handle with a layer in MLA's per-head form (create it
  * with LLATTE_ATTN_ABSORBED), with d_time > 0 (the code of an event changes with the
  * request), with d_out > 0 (the mean is over rows that are not computed again),
- * or whose layers drop rows.  Faults in the caches' arguments go to their own
+ * or whose layers drop rows that a cache holds (give its max_pages, or the table, no
+ * more pages than K events take).  Faults in the caches' arguments go to their own
  * status words.  Asynchronous on `stream`.
  */
 typedef struct {

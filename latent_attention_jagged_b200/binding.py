@@ -432,7 +432,9 @@ class Llatte:
         """A forward pass whose `values` are only the new events of every user: layer l
         appends their latents to caches[l] and attends over it.  tables: one page
         table, or one per layer; lengths: cached events, the new ones included.
-        The layers must keep every row (see llatte_forward_cached)."""
+        Every layer must keep every cached event: no cache may hold (max_pages, or the
+        table's width) more pages than min(keep) events take, and a user with more
+        than min(keep) events is left out (see llatte_forward_cached)."""
         if getattr(self.dims, "d_time", 0):      # the code of an event changes with the request
             raise LlatteError(LLATTE_ERR_UNSUPPORTED, "llatte_forward_cached")
         B = self._check_inputs(values, offsets, context, cand, None)

@@ -647,12 +647,16 @@ cudaError_t run_attn(llatte_cache* h, const CacheAttn& a, cudaStream_t s) {
 namespace llatte {
 
 int cache_layer_check(const llatte_cache* h, const llatte_cache_view* v, int heads, int rank,
-                      int dtype, int64_t rows_q, int accumulate) {
+                      int dtype, int64_t rows_q, int accumulate, int keep) {
   const int rc = check_view(h, v);
   if (rc != LLATTE_OK) return rc;
   if (h->dims.heads != heads || h->dims.rank != rank || h->dims.dtype != dtype ||
       h->dims.max_rows < rows_q || (accumulate && !h->mass))
     return LLATTE_ERR_ARG;
+  // a history that some layer of one whole pass would cut must not fit into the pages
+  // (but for the end of the last one: the kernels look at every user's length)
+  const int64_t page = h->dims.page_size, pages = std::min(v->table_stride, h->dims.max_pages);
+  if (v->B > 0 && pages > (keep + page - 1) / page) return LLATTE_ERR_UNSUPPORTED;
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return LLATTE_ERR_CUDA;
   return dev == h->device ? LLATTE_OK : LLATTE_ERR_ARG;
@@ -664,10 +668,12 @@ int cache_layer_run(llatte_cache* h, const llatte_cache_view* v, const CacheLaye
     ++*launched;
     CacheAppend ap = {};
     ap.c = make_call(h, v, l.hoff, l.rows_h);
+    ap.c.cap = std::min<int64_t>(ap.c.cap, l.keep);
     ap.pool = h->pool; ap.mass = h->mass; ap.x = l.C;
     if (launch_cache_append(h->elem, ap, s) != cudaSuccess) return LLATTE_ERR_CUDA;
   }
   CacheAttn a = make_attn(h, v, l.q, l.qoff, l.rows_q, l.out);
+  a.c.cap = std::min<int64_t>(a.c.cap, l.keep);
   a.c.n_cand = l.n_cand; a.c.window = l.window; a.c.n_sink = l.n_sink;
   a.lse2 = l.accumulate ? h->lse2 : nullptr;
   a.scale2 = l.scale2;

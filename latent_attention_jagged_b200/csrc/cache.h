@@ -60,11 +60,12 @@ struct CacheLayer {
   const void* q; const int64_t* qoff; int64_t rows_q;    // [rows_q, h, r]
   void* out;
   int64_t pairs;             // estimate of the pairs in use
+  int32_t keep;              // most events of a user that every layer keeps
   int32_t n_cand, window, n_sink, accumulate;
   float scale2;              // scores in log2 units = scale2 * q . c
 };
 int cache_layer_check(const llatte_cache* h, const llatte_cache_view* v, int heads, int rank,
-                      int dtype, int64_t rows_q, int accumulate);
+                      int dtype, int64_t rows_q, int accumulate, int keep);
 int cache_layer_run(llatte_cache* h, const llatte_cache_view* v, const CacheLayer& a,
                     int* launched, cudaStream_t s);
 

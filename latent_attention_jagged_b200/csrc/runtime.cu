@@ -859,6 +859,7 @@ int forward_impl(llatte_handle* h, const void* values, const int64_t* offsets, i
       a.pairs = (h->max_rows_q + D.max_batch - 1) / D.max_batch * B * D.heads;
       a.n_cand = D.n_q; a.window = fc->window; a.n_sink = fc->n_sink;
       a.accumulate = fc->accumulate;
+      a.keep = *std::min_element(D.keep, D.keep + L);
       a.scale2 = tc ? 1.f : 1.4426950408889634f;   // log2 e is folded into the tensor-core q~
       int launched = 0;
       const int rc = cache_layer_run(fc->caches[l], &fc->views[l], a, &launched, s);
@@ -1071,12 +1072,16 @@ int llatte_forward_cached(llatte_handle* h, const llatte_batch* b, const llatte_
   if (fc->window < 0 || fc->n_sink < 0 || (fc->accumulate != 0 && fc->accumulate != 1))
     return LLATTE_ERR_ARG;
   if (h->heads_mask != 0 || D.d_time > 0 || D.d_out > 0) return LLATTE_ERR_UNSUPPORTED;
+  // Layers that drop rows of a history would attend over events that one pass over the
+  // whole history hides from them.  max_len bounds the new events only; what a history
+  // may grow to is checked against every layer's cache.
+  const int keep = *std::min_element(D.keep, D.keep + D.n_layers);
+  if (keep < D.max_len) return LLATTE_ERR_UNSUPPORTED;
   for (int l = 0; l < D.n_layers; ++l) {
-    if (D.keep[l] < D.max_len) return LLATTE_ERR_UNSUPPORTED;
     const llatte_cache_view* v = &fc->views[l];
     if (v->B != b->B) return LLATTE_ERR_ARG;
     const int rc = cache_layer_check(fc->caches[l], v, D.heads, D.rank, D.dtype, h->max_rows_q,
-                                     fc->accumulate);
+                                     fc->accumulate, keep);
     if (rc != LLATTE_OK) return rc;
   }
   return forward_impl(h, b->values, b->offsets, b->B, b->context, b->cand, nullptr, out, stream, fc);
