@@ -473,7 +473,8 @@ void llatte_tokenizer_destroy(llatte_tokenizer* tok);
  * user whose offsets decrease, are negative or pass the rows given, or who has
  * more new rows than cached events (LLATTE_DEV_BAD_OFFSETS), or whose length is
  * negative or above its pages (LLATTE_DEV_TOO_LONG), is left out of the call
- * (in llatte_cache_append its neighbours' rows may be left out with it);
+ * (in llatte_cache_append its neighbours' rows may be left out with it; in
+ * llatte_cache_attend the rows that good offsets name get out = 0, lse = -infinity);
  * a page id outside the pool (LLATTE_DEV_BAD_ID) reads as zero rows and is
  * never written.  In llatte_cache_attend a page none of whose events any row sees is
  * not looked at: its
@@ -602,7 +603,8 @@ int llatte_cache_evict(llatte_cache* cache, const llatte_cache_view* view,
  * to its cache and attends over that.  Every layer must keep every cached event: with
  * K = the smallest keep[l], max_len (which bounds the new events here) may not exceed K,
  * no layer's pages may hold more than K events (rounded up to whole pages), and a
- * user whose length exceeds K is left out (LLATTE_DEV_TOO_LONG).  The result is then
+ * user whose length exceeds K is left out (LLATTE_DEV_TOO_LONG).  For a user that a
+ * layer's cache leaves out that layer's attention gives zeros.  The result is then
  * llatte_forward's on the whole histories; after eviction, or with a window, it is the
  * attention over what is left.  The context must be the one the cached events were
  * computed with.

@@ -627,6 +627,7 @@ CacheAttn make_attn(const llatte_cache* h, const llatte_cache_view* v, const voi
                     const int64_t* qoff, int64_t rows, void* out) {
   CacheAttn a = {};
   a.c = make_call(h, v, qoff, rows);
+  a.c.zero_left_out = 1;     // no row that a user's offsets name keeps an earlier call's bits
   a.pool = h->pool; a.mass = h->mass; a.q = q; a.out = out;
   a.part_o = h->part_o; a.part_ml = h->part_ml; a.join = h->join;
   a.count = h->parts;

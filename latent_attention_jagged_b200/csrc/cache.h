@@ -23,6 +23,7 @@ struct CacheCall {
   uint32_t head_mul;         // division by heads (cache_div); 0 for one head
   int32_t head_shift;
   int32_t n_cand, window, n_sink;
+  int32_t zero_left_out;     // rows of a user left out for its length become zeros
   int32_t* status;
 };
 

@@ -23,23 +23,29 @@ __device__ __forceinline__ int32_t cache_div(const CacheCall& c, uint32_t n) {
 
 // A user of the call from its offsets and length; a user the header leaves out
 // (bad offsets or length) gets no rows and no events, and its fault goes to the
-// status word.
+// status word.  With zero_left_out it keeps the rows that good offsets name, as rows
+// that see nothing.
 __device__ __forceinline__ CacheUser cache_user_of(const CacheCall& c, int64_t a, int64_t b,
                                                    int32_t len) {
   CacheUser x = {0, 0, 0, 0};
   int bad = (len < 0 || len > c.cap) ? LLATTE_DEV_TOO_LONG : 0;
-  if (a < 0 || b < a || b > c.rows) bad |= LLATTE_DEV_BAD_OFFSETS;
+  const bool named = !(a < 0 || b < a || b > c.rows);
+  if (!named) bad |= LLATTE_DEV_BAD_OFFSETS;
   if (!bad) {
     x.row0 = a;
     x.n = (int32_t)(b - a);
     x.m = max(0, x.n - c.n_cand);
     x.len = len;
-    if (x.m > len) {
-      bad = LLATTE_DEV_BAD_OFFSETS;
-      x = {0, 0, 0, 0};
+    if (x.m > len) bad = LLATTE_DEV_BAD_OFFSETS;
+  }
+  if (bad) {
+    atomicOr(c.status, bad);
+    x = {0, 0, 0, 0};
+    if (named && c.zero_left_out) {
+      x.row0 = a;
+      x.n = (int32_t)(b - a);
     }
   }
-  if (bad) atomicOr(c.status, bad);
   return x;
 }
 

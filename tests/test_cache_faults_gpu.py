@@ -1,0 +1,43 @@
+"""What callers of the paged cache get back for users that a call leaves out."""
+import numpy as np
+import pytest
+import torch
+
+import oracle.cache as oc
+from cache_harness import Case, attend_bounds, close
+from latent_attention_jagged_b200.binding import DEV_BAD_OFFSETS, DEV_TOO_LONG
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype,rank", [("bf16", 128), ("bf16", 40), ("fp32", 32), ("fp32", 256)])
+@pytest.mark.parametrize("new", [1, 40])
+def test_rows_of_users_left_out_are_zeros(dtype, rank, new):
+    c = Case(dtype, 4, rank, 32, [70, 130, 64, 90], seed=7)
+    q, off = c.queries([new] * 4, 1)
+    ref, ref_lse = oc.attend(c.host_pool(), None, q.double().cpu().numpy(), off, c.table,
+                             c.lengths, 1, 0.1)
+    lengths = c.lengths.copy()
+    lengths[1], lengths[2] = 1 << 20, -1
+    if new == 1:
+        lengths[3] = 0                       # fewer events than new rows
+    out, lse = torch.full_like(q, 3.0), torch.full(q.shape[:2], 3.0, device="cuda")
+    before = c.mass.clone()
+    c.cache.attend(q, torch.from_numpy(off).cuda(), c.dev("table"),
+                   torch.from_numpy(lengths).cuda(), n_cand=1, scale=0.1, out=out, lse=lse,
+                   accumulate=True)
+    assert c.cache.status() == DEV_TOO_LONG | (DEV_BAD_OFFSETS if new == 1 else 0)
+    left = [1, 2] + ([3] if new == 1 else [])
+    for u in range(4):
+        a, b = off[u], off[u + 1]
+        pages = torch.from_numpy(c.table[u][:-(-int(c.lengths[u]) // 32)]).long().cuda()
+        if u in left:
+            assert (out[a:b] == 0).all() and (lse[a:b] == -float("inf")).all()
+            assert torch.equal(c.mass[pages], before[pages])
+        else:
+            sp = {}
+            oc.attend(c.host_pool(), None, q.double().cpu().numpy(), off, c.table, c.lengths, 1,
+                      0.1, 0, 0, sp)
+            b_out, b_lse = attend_bounds(dtype, rank, 130, sp, ref, ref_lse)
+            close(out[a:b], ref[a:b], b_out[a:b], "out")
+            close(lse[a:b], ref_lse[a:b], b_lse[a:b], "lse")

@@ -1,5 +1,6 @@
 """The forward pass over cached histories where it has to refuse or to leave a user
-out: models whose layers drop rows, and histories longer than the layers keep."""
+out: models whose layers drop rows, histories longer than the layers keep, and users
+whose length or pages are wrong."""
 import dataclasses
 
 import numpy as np
@@ -8,7 +9,9 @@ import torch
 
 import oracle
 from latent_attention_jagged_b200 import LatentCache, LlatteError
-from latent_attention_jagged_b200.binding import DEV_TOO_LONG, LLATTE_ERR_UNSUPPORTED
+from latent_attention_jagged_b200.binding import (DEV_BAD_OFFSETS, DEV_TOO_LONG,
+                                                  LLATTE_ERR_UNSUPPORTED)
+from oracle.model import rmsnorm, silu
 
 from gpu_harness import assert_close
 from test_forward_cached_gpu import Served, _inputs
@@ -78,4 +81,53 @@ def test_a_history_longer_than_the_layers_keep_is_left_out():
     out = _call(s, [300, 50], [301, 50]).double().cpu().numpy()
     assert s.h.status() == 0 and all(c.status() == DEV_TOO_LONG for c in s.caches)
     assert all(torch.equal(c.pool, p) for c, p in zip(s.caches, pools))     # nothing appended
+    assert np.abs(out[0] - _without_attention(inp, 0)).max() < 0.03
     assert_close(out[1:], ref[1:], "bf16", "the user beside it")
+
+
+def _without_attention(inp, u):
+    """fp64 layers of a user's query tokens when the attention gives zeros."""
+    D, Y = inp.dims, inp.cand[u].astype(np.float64)
+    for w in inp.layers:
+        f = {k: np.asarray(v, np.float64) for k, v in w.items() if v is not None}
+        Z = rmsnorm(Y, f["g1"], D.eps)
+        Y = rmsnorm(Z + silu(Z @ f["W1"].T) @ f["W2"].T, f["g2"], D.eps)
+    return Y
+
+
+@pytest.mark.parametrize("dtype,kw", [
+    ("bf16", {}), ("bf16", dict(rank=40)), ("fp32", dict(rank=32))])
+@pytest.mark.parametrize("max_new", [2, 60])
+def test_rows_of_a_user_left_out_hold_nothing_of_earlier_calls(dtype, kw, max_new):
+    # a handle for a few new rows (the form for single tokens) and one for many
+    if max_new == 2:
+        kw = dict(kw, n_q=2, heads=2, d_head=64)
+    inp = _inputs(dtype, lengths=[60, 80, 50, 33], **kw)
+    n = [int(x) for x in inp.lengths]
+    old = [x - 2 for x in n]
+    s = Served(inp, max_new=max_new)
+    a = [0] * 4
+    while a != old:
+        b = [min(x + max_new, y) for x, y in zip(a, old)]
+        _call(s, a, b)
+        a = b
+    wrong = list(n)
+    wrong[1], wrong[2] = 1 << 20, 1             # beyond its pages; fewer than its new rows
+    outs = []
+    for before in (old, [x - 1 for x in old]):  # two calls that leave other rows behind
+        s.cand.mul_(-1)
+        _call(s, before, [x + 1 for x in before])
+        s.cand.copy_(torch.from_numpy(inp.cand).cuda().to(s.dt))
+        torch.cuda.synchronize()
+        assert s.h.status() == 0 and all(c.status() == 0 for c in s.caches)
+        outs.append(_call(s, old, n, lengths=wrong))
+        torch.cuda.synchronize()
+        assert all(c.status() == DEV_TOO_LONG | DEV_BAD_OFFSETS for c in s.caches)
+        assert s.h.status() == 0
+    assert torch.equal(outs[0], outs[1])
+    got = outs[0].double().cpu().numpy()
+    tol = 0.03 if dtype == "bf16" else 1e-4
+    for u in (1, 2):
+        assert np.abs(got[u] - _without_attention(inp, u)).max() < tol
+    ref = oracle.forward(inp)
+    assert_close(got[[0, 3]], ref[[0, 3]], dtype, "users beside those left out")
