@@ -4,6 +4,7 @@ every step of the forward runs in the library's kernels).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -262,6 +263,24 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+def _made(make, stream, device):
+    """make(), a tensor for a call on `stream` (None: the current stream; else a torch
+    stream or its address).  It comes from that stream's memory, whose earlier uses the
+    call follows in order; memory of the current stream may still be written by work that
+    the call does not wait for.  The caller reads it on the current stream."""
+    if stream is None:
+        return make()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream_ptr(stream).value or 0, device=device)
+    here = torch.cuda.current_stream(device)
+    if stream.cuda_stream == here.cuda_stream:
+        return make()
+    with torch.cuda.stream(stream):
+        t = make()
+    t.record_stream(here)
+    return t
+
+
 class Llatte:
     """A forward handle: weights (non-absorbed, pages' layout) are copied and
     absorbed at construction; `forward` runs the whole sequence module."""
@@ -355,9 +374,10 @@ class Llatte:
             raise ValueError("event_age [rows] (hours before the request) is required")
         return B
 
-    def _out(self, out, B, device):
+    def _out(self, out, B, device, stream=None):
         if out is None:
-            return torch.empty(self.out_shape(B), dtype=torch.float32, device=device)
+            return _made(lambda: torch.empty(self.out_shape(B), dtype=torch.float32,
+                                             device=device), stream, device)
         if (tuple(out.shape) != self.out_shape(B) or out.dtype != torch.float32
                 or not out.is_contiguous()):
             raise ValueError(f"out must be a contiguous float32 {self.out_shape(B)} tensor")
@@ -386,7 +406,7 @@ class Llatte:
         """One forward pass.  event_age (float32 [rows], hours before the
         request of every history event) is required when dims.d_time > 0."""
         B = self._check_inputs(values, offsets, context, cand, event_age)
-        out = self._out(out, B, values.device)
+        out = self._out(out, B, values.device, stream)
         if not getattr(self.dims, "d_time", 0):
             event_age = None
         self._run(values, offsets, context, cand, event_age, out, None, stream, B)
@@ -402,18 +422,19 @@ class Llatte:
         d = self.dims
         B = self._check_inputs(values, offsets, context, cand, event_age)
         dev = values.device
-        recent = torch.empty((B, d.n_q, d.heads, n_k), dtype=torch.float32, device=dev)
-        topk = torch.empty_like(recent)
-        hours = None
-        if n_hours:
-            if event_age is None:
-                raise ValueError("event_age is required for hour bins")
-            hours = torch.empty((B, d.n_q, d.heads, n_hours), dtype=torch.float32, device=dev)
+        if n_hours and event_age is None:
+            raise ValueError("event_age is required for hour bins")
+
+        def made(n):
+            return _made(lambda: torch.empty((B, d.n_q, d.heads, n), dtype=torch.float32,
+                                             device=dev), stream, dev)
+        recent, topk = made(n_k), made(n_k)
+        hours = made(n_hours) if n_hours else None
         ex = llatte_attn_export(layer=layer, n_k=n_k, n_hours=n_hours,
                                 event_age=event_age.data_ptr() if n_hours else None,
                                 recent=recent.data_ptr(), topk=topk.data_ptr(),
                                 hours=hours.data_ptr() if hours is not None else None)
-        out = self._out(out, B, dev)
+        out = self._out(out, B, dev, stream)
         self._run(values, offsets, context, cand,
                   event_age if getattr(d, "d_time", 0) else None, out, ex, stream, B)
         return out, recent, topk, hours
@@ -449,7 +470,7 @@ class Llatte:
         views = (llatte_cache_view * n)(*[c._view(t, lengths)[0] for c, t in zip(caches, tables)])
         if any(v.B != B for v in views):
             raise ValueError(f"tables and lengths must have {B} users")
-        out = self._out(out, B, values.device)
+        out = self._out(out, B, values.device, stream)
         b = llatte_batch(values=values.data_ptr(), offsets=offsets.data_ptr(), B=B,
                          context=context.data_ptr() if context is not None else None,
                          cand=cand.data_ptr() if cand is not None else None, event_age=None)
@@ -686,13 +707,8 @@ class LatentCache:
             self._refuse("table", torch.int32, f"{B}, *")
         return llatte_cache_view(table.data_ptr(), table.shape[1], lengths.data_ptr(), B), B
 
-    def _on(self, stream, made=None):
-        """The stream a call runs on; a tensor made here for it is kept until it is done."""
-        if stream is None:
-            return _raw_stream(self.index)
-        if made is not None and isinstance(stream, torch.cuda.Stream):
-            made.record_stream(stream)
-        return _stream_ptr(stream)
+    def _on(self, stream):
+        return _raw_stream(self.index) if stream is None else _stream_ptr(stream)
 
     def append(self, x: torch.Tensor, offsets: torch.Tensor, table: torch.Tensor,
                lengths: torch.Tensor, gain: Optional[torch.Tensor] = None, eps: float = 1e-6,
@@ -729,9 +745,8 @@ class LatentCache:
         rows = q.shape[0]
         if not self._fits(q_offsets, torch.int64, 1) or q_offsets.shape[0] != B + 1:
             self._refuse("q_offsets", torch.int64, B + 1)
-        made = None
         if out is None:
-            out = made = torch.empty_like(q)
+            out = _made(lambda: torch.empty_like(q), stream, self.device)
         elif not self._fits(out, self.dt, 3) or out.shape != q.shape:
             self._refuse("out", self.dt, f"{rows}, {self.heads}, {self.rank}")
         if lse is not None and (not self._fits(lse, torch.float32, 2)
@@ -741,7 +756,7 @@ class LatentCache:
                               n_sink, out.data_ptr(), None if lse is None else lse.data_ptr(),
                               1 if accumulate else 0)
         rc = self.lib.llatte_cache_attend(self.h, ctypes.byref(v), ctypes.byref(a),
-                                          self._on(stream, made))
+                                          self._on(stream))
         if rc != LLATTE_OK:
             raise LlatteError(rc, "llatte_cache_attend")
         return out
@@ -755,9 +770,8 @@ class LatentCache:
         of dst_table (default: the user's own first pages).  Returns the new
         lengths; `kept` (int32 [B, budget]) receives the old slots."""
         v, B = self._view(table, lengths)
-        made = None
         if new_lengths is None:
-            new_lengths = made = torch.empty_like(lengths)
+            new_lengths = _made(lambda: torch.empty_like(lengths), stream, self.device)
         elif not self._fits(new_lengths, torch.int32, 1) or new_lengths.shape[0] != B:
             self._refuse("new_lengths", torch.int32, B)
         if dst_table is not None and (not self._fits(dst_table, torch.int32, 2)
@@ -771,7 +785,7 @@ class LatentCache:
             0 if dst_table is None else dst_table.shape[1], new_lengths.data_ptr(),
             None if kept is None else kept.data_ptr())
         rc = self.lib.llatte_cache_evict(self.h, ctypes.byref(v), ctypes.byref(a),
-                                         self._on(stream, made))
+                                         self._on(stream))
         if rc != LLATTE_OK:
             raise LlatteError(rc, "llatte_cache_evict")
         return new_lengths
