@@ -580,7 +580,8 @@ int llatte_cache_attend(llatte_cache* cache, const llatte_cache_view* view,
  *   budget        >= 1;  n_sink + n_recent <= budget
  *   dst_table     device int32 [B, dst_stride] of pages that no other row of
  *                 either table names, or NULL
- *   new_lengths   device int32 [B], may be the view's lengths
+ *   new_lengths   device int32 [B], may be the view's lengths; the entries of users
+ *                 left out stay as they were
  *   kept          device int32 [B, budget] or NULL: the old slots of the kept
  *                 events, ascending; entries past the new length are left as
  *                 they were

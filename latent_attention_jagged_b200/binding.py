@@ -768,10 +768,11 @@ class LatentCache:
         """Keep at most `budget` events per user: the first n_sink, the last n_recent
         and the heaviest of the others by `mass`, packed in order into the pages
         of dst_table (default: the user's own first pages).  Returns the new
-        lengths; `kept` (int32 [B, budget]) receives the old slots."""
+        lengths; `kept` (int32 [B, budget]) receives the old slots.  A user left out
+        (see the status) keeps what new_lengths held, by default the length given."""
         v, B = self._view(table, lengths)
-        if new_lengths is None:
-            new_lengths = _made(lambda: torch.empty_like(lengths), stream, self.device)
+        if new_lengths is None:              # a user left out keeps its length
+            new_lengths = _made(lambda: lengths.clone(), stream, self.device)
         elif not self._fits(new_lengths, torch.int32, 1) or new_lengths.shape[0] != B:
             self._refuse("new_lengths", torch.int32, B)
         if dst_table is not None and (not self._fits(dst_table, torch.int32, 2)

@@ -10,6 +10,22 @@ from latent_attention_jagged_b200.binding import DEV_BAD_OFFSETS, DEV_TOO_LONG
 pytestmark = pytest.mark.gpu
 
 
+@pytest.mark.parametrize("budget", [8, 100])
+@pytest.mark.parametrize("apart", [False, True])
+def test_lengths_that_eviction_returns_for_users_left_out(budget, apart):
+    c = Case("bf16", 2, 64, 16, [40, 40, 40, 5], seed=13, spare=16, stale=0.25)
+    lengths = c.lengths.copy()
+    lengths[0], lengths[1] = -5, 10 ** 6
+    dst = torch.tensor(c.free[:12], dtype=torch.int32).reshape(4, 3).cuda() if apart else None
+    for _ in range(3):                       # blocks of freed memory hold other numbers
+        junk = torch.full((4,), 23, dtype=torch.int32, device="cuda")
+        del junk
+        got = c.cache.evict(c.dev("table"), torch.from_numpy(lengths).cuda(), budget,
+                            dst_table=dst)
+        assert c.cache.status() == DEV_TOO_LONG
+        assert got.cpu().tolist() == [-5, 10 ** 6, min(40, budget), 5]
+
+
 @pytest.mark.parametrize("dtype,rank", [("bf16", 128), ("bf16", 40), ("fp32", 32), ("fp32", 256)])
 @pytest.mark.parametrize("new", [1, 40])
 def test_rows_of_users_left_out_are_zeros(dtype, rank, new):
