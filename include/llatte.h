@@ -462,7 +462,11 @@ void llatte_tokenizer_destroy(llatte_tokenizer* tok);
  *   dtype           LLATTE_BF16 or LLATTE_FP32, of pool, queries and outputs
  *                   (sums, softmax statistics and masses are fp32); bf16 with
  *                   r = 64, 128 or 256 runs on the tensor cores, where the
- *                   weights are rounded to bf16 before their product with c
+ *                   weights are rounded to bf16 before their product with c and
+ *                   their sum is not (an error of up to 2^-8 of every weight).
+ *                   Calls of at most 16 rows x heads a user (on average) are
+ *                   exact to 2^-16 for users of up to 8, and others of theirs
+ *                   divide by the sum of the rounded weights
  *   page_size       16, 32, 64 or 128
  *   n_pages         pages of the pool, n_pages * page_size < 2^31
  *   max_batch       most users of one call (<= LLATTE_CACHE_MAX_BATCH)

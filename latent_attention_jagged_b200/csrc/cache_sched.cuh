@@ -15,10 +15,10 @@
 
 namespace llatte {
 
-// Growth of a row's maximum (log2 units) up to which its sums keep their base.  bf16
-// weights and fp32 sums keep their relative precision at any base; the base only has
-// to keep them in range: weights up to 2^20 leave latents up to 2^70 and 2^31 events
-// room.  With 2^8 some row of a block outgrew its first 64 events in many items, and
+// Growth of a row's maximum (log2 units) up to which its sums keep their base.  Any base
+// leaves a weight the same relative rounding (2^-8 in bf16; only at the running maximum
+// would the largest weight, 1, have none), so that the base only has to keep sums in
+// range: weights up to 2^20 leave latents up to 2^70 and 2^31 events room.  With 2^8 some row of a block outgrew its first 64 events in many items, and
 // a rescale waits for every product before it (64 candidates for 256 users: 44.3 us).
 constexpr float kGrow = 20.f;
 

@@ -1,8 +1,8 @@
 // Attention of few new rows over the paged latent cache (bf16, rank 64, 128 or 256):
 // the form for single tokens.
 //
-// With 16 (query row, head) pairs or fewer the work is bound by reading the cache: 4 r
-// flops per pair and event against 2 r bytes.  The 128-row tensor-memory products of
+// With 16 (query row, head) pairs or fewer the floor is reading the cache: 4 r flops per
+// pair and event against 2 r bytes.  The 128-row tensor-memory products of
 // cache_attn_sm100.cu would run on padding, and every tile would wait for the chain
 // S -> softmax -> P C; here the warps do not wait for one another at all.  A block of
 // 16 pairs is one m16 operand; of a tile of 128 events each of 8 warps takes 16, with
@@ -10,10 +10,11 @@
 // weights never leave them), and the 8 results meet once per item.  A ninth warp keeps
 // 192 KB of tiles on their way.
 //
-// Measured (64 users, 2000 to 8000 events, 8 heads, rank 256: 159 MB): 50 us, the
-// steady state at 2500 cycles per 64 KB tile and SM (6.9 TB/s); what is left is the
-// beginning (the split and the first loads: 5 us), the meeting and the joining of cut
-// blocks at the end (5 us), and the launch.
+// Measured (64 users, 2000 to 8000 events, 8 heads, rank 256: 159 MB): 45 us, half the
+// rate of HBM.  Its loads do not bound it (DRAM 37 % busy, tensor pipe 24 %, issue slots
+// 20 % in the kernel at 48 us): each of two warps a scheduler waits for its own chain of
+// ldmatrix, products and softmax, 64 products a tile of which half are padding at 8
+// pairs.
 #include <cuda.h>
 
 #include <algorithm>
@@ -36,10 +37,16 @@ constexpr int MT = 16;                    // pairs of a block
 constexpr int KT = 128;                   // events of a tile
 constexpr int NW = 8;                     // consumer warps, 16 events of a tile each
 // Three warpgroups, the third for the producer: the launch's 168 registers a thread
-// are dealt out again, 128 threads x (232 + 232 + 40) = 384 x 168.
+// are dealt out again, 128 threads x (232 + 232 + 40) = 384 x 168.  At r = 256 queries
+// and results alone take 192, and what does not fit is read back from local memory in
+// every tile (with all of shared memory in use little of it stays in L1), so that the
+// consumers take 240 and leave the producer 24 (64 users of 2000 to 8000 events, 8 heads:
+// 48 -> 45 us; at r = 128 the producer's own spills cost more, 29 -> 30 us).
 constexpr int kThreads = 384;
-constexpr int kRegsConsume = 232, kRegsProduce = 40;
-static_assert(2 * kRegsConsume + kRegsProduce <= 504, "registers of the launch");
+template <int R> constexpr int kRegsConsume = R == 256 ? 240 : 232;
+template <int R> constexpr int kRegsProduce = R == 256 ? 24 : 40;
+static_assert(2 * kRegsConsume<128> + kRegsProduce<128> <= 504 &&
+              2 * kRegsConsume<256> + kRegsProduce<256> <= 504, "registers of the launch");
 
 template <int R>
 struct Cfg {
@@ -49,7 +56,7 @@ struct Cfg {
   static constexpr uint32_t KV_BYTES = RSUB * KV_SUB;
   static constexpr uint32_t MEET = NW * MT * 64 * 4;   // 64 columns of every warp's result
   static constexpr uint32_t BAR_BYTES = 512;
-  static constexpr size_t SMEM = 1024 + KS * KV_BYTES + MEET + BAR_BYTES + 2 * NW * MT * 4;
+  static constexpr size_t SMEM = 1024 + KS * KV_BYTES + MEET + BAR_BYTES + 3 * NW * MT * 4;
   static_assert(SMEM <= 232448, "shared memory budget");
   static_assert(KS * KV_BYTES >= sizeof(CacheSplitSpace), "split");
 };
@@ -78,6 +85,11 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The two bf16 numbers of a register in fp32.
+__device__ __forceinline__ float2 unpack_bf16(uint32_t p) {
+  return make_float2(__uint_as_float(p << 16), __uint_as_float(p & 0xffff0000u));
 }
 
 // The warp clears the latents of its 16 events that are not finite.
@@ -122,6 +134,7 @@ cache_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn p) {
   static_assert((2 * KS + 2) * 8 + sizeof(CacheSplit) <= C::BAR_BYTES, "barriers");
   float* sm_m = (float*)((uint8_t*)bars + C::BAR_BYTES);   // [NW][MT]
   float* sm_l = sm_m + NW * MT;
+  float* sm_r = sm_l + NW * MT;
 
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -139,7 +152,7 @@ cache_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn p) {
   const CacheSplit run = *split;
 
   if (warp >= NW) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsProduce));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsProduce<R>));
     if (warp == NW) {
     CacheItems<Line> items;
     items.start(c, run);
@@ -188,7 +201,7 @@ cache_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn p) {
     __syncwarp();
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsConsume));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsConsume<R>));
     CacheItems<Line> items;
     items.start(c, run);
     CacheItem<Line> it;
@@ -205,6 +218,7 @@ cache_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn p) {
       const int64_t pair0 = (int64_t)it.b * MT;
       const int32_t rows = (int32_t)min((int64_t)MT, (int64_t)it.x.n * c.heads - pair0);
       const int64_t at0 = it.x.row0 * c.heads + pair0;
+      const bool few = rows <= 8;
       if (it.x.len == 0) {                 // no event: zeros
         for (int i = threadIdx.x; i < rows * (R / 8); i += 32 * NW)
           ((uint4*)((__nv_bfloat16*)p.out + at0 * R))[i] = make_uint4(0, 0, 0, 0);
@@ -236,7 +250,8 @@ cache_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn p) {
       float o[R / 8][4];
 #pragma unroll
       for (int k = 0; k < R / 8; ++k) o[k][0] = o[k][1] = o[k][2] = o[k][3] = 0.f;
-      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      // maximum, sum of the weights and of the rounded ones
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, lr[2] = {0.f, 0.f};
       for (int i = it.t0; ok && i < it.t1; ++i, ++g) {
         const int st = g % KS;
         bool w = mbar_wait(&kv_full[st], (g / KS) & 1, abort_flag, c.status);
@@ -249,24 +264,24 @@ cache_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn p) {
         }
         uint8_t* kv = sKV + st * C::KV_BYTES;
         const uint32_t kv_addr = smem_u32(kv);
-        // S = Q C^T: two accumulators of 16 pairs x 8 events, even and odd steps apart
-        float s[2][2][4];
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[0][j][e] = s[1][j][e] = 0.f;
-#pragma unroll
-        for (int k = 0; k < R / 16; ++k) {
-          uint32_t b[4];
-          ldsm4(kv_addr + (k >> 2) * C::KV_SUB + k_row + (((2 * (k & 3) + k_chunk) ^ xr) << 4), b);
-          mma16816(s[k & 1][0], qa[k], b[0], b[1]);
-          mma16816(s[k & 1][1], qa[k], b[2], b[3]);
-        }
+        // S = Q C^T: 16 pairs x 8 events twice (even and odd steps in accumulators of their
+        // own cost 8 registers more than they gain)
         float v[2][4];                     // [event group j][row half * 2 + event]
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[j][e] = (s[0][j][e] + s[1][j][e]) * p.scale2;
+          for (int e = 0; e < 4; ++e) v[j][e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < R / 16; ++k) {
+          uint32_t b[4];
+          ldsm4(kv_addr + (k >> 2) * C::KV_SUB + k_row + (((2 * (k & 3) + k_chunk) ^ xr) << 4), b);
+          mma16816(v[0], qa[k], b[0], b[1]);
+          mma16816(v[1], qa[k], b[2], b[3]);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[j][e] *= p.scale2;
         bool poison[2] = {false, false};
         if (it.k.pmin < t0 + 15 || low_max > t0) {
           // some row hides some of the 16 events
@@ -299,23 +314,34 @@ cache_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn p) {
           grow |= mt[h] > m[h] + kGrow;
         }
         if (__any_sync(0xffffffffu, grow)) {
+          float f[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const float mn = fmaxf(m[h], mt[h]);
-            const float f = m[h] > -INFINITY ? ex2_approx(m[h] - mn) : 0.f;
+            f[h] = m[h] > -INFINITY ? ex2_approx(m[h] - mn) : 0.f;
             m[h] = mn;
-            l[h] *= f;
+            l[h] *= f[h];
+            lr[h] *= f[h];
+          }
+          if (few) f[1] = f[0];
 #pragma unroll
-            for (int k = 0; k < R / 8; ++k) {
-              o[k][2 * h] *= f;
-              o[k][2 * h + 1] *= f;
-            }
+          for (int k = 0; k < R / 8; ++k) {
+            o[k][0] *= f[0];
+            o[k][1] *= f[0];
+            o[k][2] *= f[1];
+            o[k][3] *= f[1];
           }
         }
-        // weights, in bf16 for the product and unrounded in the sum
+        // Weights.  For the product they are rounded to bf16.  Where rows 8 to 15 of the
+        // operand are free what the rounding took goes there, rounded too, and the halves
+        // of the result are added at the end: weights are then off by 2^-16 at most, for no
+        // product more.  With more rows the result is divided by the sum of the rounded
+        // weights, so that only their spread is left of the error (a second product for
+        // the rests: 64 users of 2000 to 8000 events, 16 heads, r = 256, 59 -> 69 us).
+        // The log sum is always that of the unrounded ones.
         uint32_t pa[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 1; h >= 0; --h) {
           const float mu = m[h] > -INFINITY ? m[h] : 0.f;
           const float a = ex2_approx(v[0][2 * h] - mu), b = ex2_approx(v[0][2 * h + 1] - mu);
           const float d = ex2_approx(v[1][2 * h] - mu), e = ex2_approx(v[1][2 * h + 1] - mu);
@@ -323,6 +349,12 @@ cache_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn p) {
           if (poison[h]) l[h] = NAN;
           pa[h] = pack_bf16(a, b);
           pa[2 + h] = pack_bf16(d, e);
+          const float2 x = unpack_bf16(pa[h]), y = unpack_bf16(pa[2 + h]);
+          if (few && h == 0) {
+            pa[1] = pack_bf16(a - x.x, b - x.y);
+            pa[3] = pack_bf16(d - y.x, e - y.y);
+          }
+          if (!few) lr[h] += (x.x + x.y) + (y.x + y.y);
         }
         // O += P C: 16 columns a step
 #pragma unroll
@@ -335,15 +367,27 @@ cache_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn p) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&kv_empty[st]);
       }
+      if (few) {
+#pragma unroll
+        for (int k = 0; k < R / 8; ++k) {
+          o[k][0] += o[k][2];
+          o[k][1] += o[k][3];
+        }
+      }
       // ---- the warps' results meet (after an abort too: every warp makes the same
       // number of meets, so none waits alone)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+        if (few) lr[h] = l[h];
+#pragma unroll
+        for (int d = 1; d <= 2; d *= 2) {
+          l[h] += __shfl_xor_sync(0xffffffffu, l[h], d);
+          lr[h] += __shfl_xor_sync(0xffffffffu, lr[h], d);
+        }
         if (t4 == 0) {
           sm_m[warp * MT + grp + 8 * h] = m[h];
           sm_l[warp * MT + grp + 8 * h] = l[h];
+          sm_r[warp * MT + grp + 8 * h] = lr[h];
         }
       }
       meet_sync();
@@ -359,18 +403,22 @@ cache_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn p) {
       // are no more than 8, of 8 rows and twice the columns.  A thread sums 4 columns
       // of a row.  Column pairs are XORed with the row, so that the 8 rows of a store
       // fall on different banks.
-      const bool few = rows <= 8;
       const int line = threadIdx.x >> 4, c4 = threadIdx.x & 15, row = few ? line & 7 : line;
-      float mall = -INFINITY, lall = 0.f;
+      float mall = -INFINITY, lall = 0.f, rall = 0.f;
 #pragma unroll
       for (int k = 0; k < NW; ++k) mall = fmaxf(mall, sm_m[k * MT + row]);
       const float mu = mall > -INFINITY ? mall : 0.f;
 #pragma unroll
-      for (int k = 0; k < NW; ++k)
-        lall = fmaf(sm_l[k * MT + row], ex2_approx(sm_m[k * MT + row] - mu), lall);
+      for (int k = 0; k < NW; ++k) {
+        const float w = ex2_approx(sm_m[k * MT + row] - mu);
+        lall = fmaf(sm_l[k * MT + row], w, lall);
+        rall = fmaf(sm_r[k * MT + row], w, rall);
+      }
       if (mall == INFINITY) lall = NAN;
       const int64_t slot = ((int64_t)blockIdx.x * 2 + (it.starts ? 1 : 0)) * MT + row;
-      const float inv = lall != 0.f ? 1.f / lall : 0.f;
+      // a whole block is divided by the sum of the rounded weights; a part becomes its mean
+      // times the sum of the unrounded ones, which is what parts are joined by
+      const float mul = lall != 0.f ? (it.whole ? 1.f : lall) / (lall == lall ? rall : NAN) : 0.f;
       auto put = [&](int unit, int q, int h) {
 #pragma unroll
         for (int k = 0; k < 8; ++k)
@@ -389,9 +437,10 @@ cache_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn p) {
           }
           if (it.whole)
             *(uint2*)((__nv_bfloat16*)p.out + (at0 + row) * R + q * 64 + c4 * 4) =
-                make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
+                make_uint2(pack_bf16(x.x * mul, x.y * mul), pack_bf16(x.z * mul, x.w * mul));
           else
-            *(float4*)(p.part_o + slot * R + q * 64 + c4 * 4) = x;
+            *(float4*)(p.part_o + slot * R + q * 64 + c4 * 4) =
+                make_float4(x.x * mul, x.y * mul, x.z * mul, x.w * mul);
         }
         meet_sync();
       };
@@ -656,7 +705,7 @@ cudaError_t launch_r(CacheAttn a, const CUtensorMap& tmC, int num_sms, cudaStrea
     cudaFuncAttributes f;
     e = cudaFuncGetAttributes(&f, cache_token_kernel<R>);
     if (e != cudaSuccess) return e;
-    if (f.numRegs * 3 < 2 * kRegsConsume + kRegsProduce) return cudaErrorInvalidConfiguration;
+    if (f.numRegs * 3 < 2 * kRegsConsume<R> + kRegsProduce<R>) return cudaErrorInvalidConfiguration;
     attr_devices |= 1ull << (dev & 63);
   }
   cache_launched(a, 1);
