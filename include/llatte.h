@@ -530,7 +530,8 @@ typedef struct {
  *   x        device [rows, rank] in dtype, 16-byte aligned
  *   offsets  device int64 [B+1], non-decreasing, offsets[B] <= rows
  *   gain     device [rank] in dtype, 16-byte aligned, or NULL
- * Asynchronous on `stream`.  Appending the same rows again changes nothing.
+ * Asynchronous on `stream`.  Appending the same rows again leaves the latents as they
+ * are, but their masses start over: what the events had collected in between is gone.
  */
 int llatte_cache_append(llatte_cache* cache, const llatte_cache_view* view, const void* x,
                         int64_t rows, const int64_t* offsets, const void* gain, float eps,
@@ -625,7 +626,9 @@ int llatte_cache_evict(llatte_cache* cache, const llatte_cache_view* view,
  * request), with d_out > 0 (the mean is over rows that are not computed again),
  * or whose layers drop rows that a cache holds (give its max_pages, or the table, no
  * more pages than K events take).  Faults in the caches' arguments go to their own
- * status words.  Asynchronous on `stream`.
+ * status words.  Asynchronous on `stream`.  The same call again gives the same `out`;
+ * with accumulate = 1 it adds to the masses of older events a second time, while those
+ * of the call's own events start over.
  */
 typedef struct {
   llatte_cache* const* caches;

@@ -714,7 +714,8 @@ class LatentCache:
                lengths: torch.Tensor, gain: Optional[torch.Tensor] = None, eps: float = 1e-6,
                stream=None):
         """Rows x[offsets[u]:offsets[u + 1]] become user u's newest events (lengths
-        counts them already); with `gain` each is RMS-normalised first."""
+        counts them already); with `gain` each is RMS-normalised first.  Their masses
+        are set to 0, also where the same rows are appended again."""
         v, B = self._view(table, lengths)
         if not self._fits(x, self.dt, 2) or x.shape[1] != self.rank:
             self._refuse("x", self.dt, f"*, {self.rank}")

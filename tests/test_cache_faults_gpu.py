@@ -1,10 +1,11 @@
-"""What callers of the paged cache get back for users that a call leaves out."""
+"""What callers of the paged cache get back for users that a call leaves out, and from
+repeated calls."""
 import numpy as np
 import pytest
 import torch
 
 import oracle.cache as oc
-from cache_harness import Case, attend_bounds, close
+from cache_harness import DT, Case, attend_bounds, close, mass_bound
 from latent_attention_jagged_b200.binding import DEV_BAD_OFFSETS, DEV_TOO_LONG
 
 pytestmark = pytest.mark.gpu
@@ -57,3 +58,33 @@ def test_rows_of_users_left_out_are_zeros(dtype, rank, new):
             b_out, b_lse = attend_bounds(dtype, rank, 130, sp, ref, ref_lse)
             close(out[a:b], ref[a:b], b_out[a:b], "out")
             close(lse[a:b], ref_lse[a:b], b_lse[a:b], "lse")
+
+
+@pytest.mark.parametrize("dtype,rank", [("bf16", 128), ("fp32", 32)])
+def test_appending_again_clears_what_the_events_collected(dtype, rank):
+    # the latents stay, the masses of the appended rows start over, those of the events
+    # before them do not
+    c = Case(dtype, 2, rank, 32, [100, 40], seed=9, stale=0.0)
+    new = [10, 3]
+    x = torch.from_numpy(c.rng.standard_normal((13, rank)).astype(np.float32)).to(DT[dtype]).cuda()
+    off = torch.tensor([0, 10, 13]).cuda()
+    args = (x, off, c.dev("table"), c.dev("lengths"))
+    c.mass.zero_()
+    c.cache.append(*args)
+    q, qoff = c.queries(new, 1)
+    sp = {}
+    mass = c.host_mass()
+    oc.attend(c.host_pool(), mass, q.double().cpu().numpy(), qoff, c.table, c.lengths, 1, 0.1, 0, 0,
+              sp)
+    c.cache.attend(q, torch.from_numpy(qoff).cuda(), c.dev("table"), c.dev("lengths"), n_cand=1,
+                   scale=0.1, accumulate=True)
+    bound = mass_bound(rank, 100, sp, mass)
+    close(c.mass, mass, bound, "mass")
+    pool = c.pool.clone()
+    c.cache.append(*args)
+    assert torch.equal(c.pool, pool) and c.cache.status() == 0
+    for u, m in enumerate(new):
+        pg, rw = oc.slots(c.table[u], int(c.lengths[u]), 32)
+        mass[pg[-m:], rw[-m:]] = 0.0
+        bound[pg[-m:], rw[-m:]] = 0.0
+    close(c.mass, mass, bound, "mass after the second append")

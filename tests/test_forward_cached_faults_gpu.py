@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import oracle
+import oracle.cache as oc
 from latent_attention_jagged_b200 import LatentCache, LlatteError
 from latent_attention_jagged_b200.binding import (DEV_BAD_OFFSETS, DEV_TOO_LONG,
                                                   LLATTE_ERR_UNSUPPORTED)
@@ -131,3 +132,21 @@ def test_rows_of_a_user_left_out_hold_nothing_of_earlier_calls(dtype, kw, max_ne
         assert np.abs(got[u] - _without_attention(inp, u)).max() < tol
     ref = oracle.forward(inp)
     assert_close(got[[0, 3]], ref[[0, 3]], dtype, "users beside those left out")
+
+
+def test_the_same_request_again():
+    # the same result; older events are counted a second time, the new ones start over
+    inp = _inputs(lengths=[130, 40])
+    s = Served(inp)
+    s.request([0, 0], [100, 39])
+    first = s.request([100, 39], [130, 40], accumulate=True)
+    once = [c.mass.double() for c in s.caches]
+    again = s.request([100, 39], [130, 40], accumulate=True)
+    assert np.array_equal(first, again)
+    for c, m in zip(s.caches, once):
+        for u, (old, n) in enumerate(((100, 130), (39, 40))):
+            at = tuple(torch.from_numpy(x).cuda() for x in oc.slots(s.table[u], n, s.page))
+            was, now = m[at], c.mass.double()[at]
+            assert torch.allclose(now[:old], 2 * was[:old], rtol=1e-5, atol=0)
+            assert torch.allclose(now[old:], was[old:], rtol=1e-5, atol=0)
+            assert (was > 0).all()
