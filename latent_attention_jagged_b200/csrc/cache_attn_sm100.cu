@@ -32,6 +32,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "cache.h"
 #include "cache_call.cuh"
@@ -788,10 +789,10 @@ cudaError_t launch_r(CacheAttn a, const CUtensorMap& tmC, int num_sms, cudaStrea
   const bool many_short = R == 256 && a.never_cut && a.c.B > num_sms;
   if (a.pairs <= 16 * (int64_t)a.c.B && !many_short)
     return launch_cache_token(a, tmC, num_sms, s);
-  static uint64_t attr_devices = 0;
+  static std::atomic<uint64_t> attr_devices{0};
   int dev = 0;
   cudaGetDevice(&dev);
-  if (!(attr_devices >> (dev & 63) & 1)) {
+  if (!(attr_devices.load() >> (dev & 63) & 1)) {
     cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<R>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
     if (e != cudaSuccess) return e;

@@ -20,6 +20,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "cache.h"
 #include "cache_call.cuh"
@@ -334,10 +335,10 @@ __global__ void __launch_bounds__(KT) cache_mass_join_kernel(const CacheAttn p) 
 template <int R>
 cudaError_t launch_rn(const CacheAttn& a, const CUtensorMap& tmC, int num_sms, cudaStream_t s) {
   using C = Cfg<R>;
-  static uint64_t attr_devices = 0;
+  static std::atomic<uint64_t> attr_devices{0};
   int dev = 0;
   cudaGetDevice(&dev);
-  if (!(attr_devices >> (dev & 63) & 1)) {
+  if (!(attr_devices.load() >> (dev & 63) & 1)) {
     cudaError_t e = cudaFuncSetAttribute(cache_mass_kernel<R>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
     if (e != cudaSuccess) return e;

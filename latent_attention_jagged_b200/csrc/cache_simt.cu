@@ -17,6 +17,7 @@
 //           2 heads, r = 32: 14 us, of which the cache's 2 MB are 0.3)
 //   mass    tiles of 64 events against all blocks of 64 pairs; a thread sums its events
 #include <algorithm>
+#include <atomic>
 
 #include "cache.h"
 #include "cache_call.cuh"
@@ -34,6 +35,7 @@ namespace {
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int MT = 64, KT = 64;           // pairs and events of a tile
 constexpr int TP = 8, TK = 32;            // the same of the token kernel
+constexpr int kSmemMax = 232448;          // shared memory of a CTA
 
 __device__ __forceinline__ float4 ld4(const float* p) { return *(const float4*)p; }
 __device__ __forceinline__ float4 ld4(const __nv_bfloat16* p) {
@@ -660,14 +662,25 @@ __global__ void __launch_bounds__(KT) cache_mass_rows_join_kernel(CacheAttn p) {
 }
 
 // ---------------------------------------------------------------- launches
-template <typename K>
-cudaError_t launch_with(K kernel, int grid, int threads, size_t smem, const CacheAttn& a,
-                        cudaStream_t s) {
+// A kernel's limit of dynamic shared memory is set once for a device, to all there is beside
+// its static part: set to each launch's own need, a call of a cache of another rank could
+// lower it between another thread's setting and its launch.
+template <void (*Kernel)(CacheAttn)>
+cudaError_t launch_with(int grid, int threads, size_t smem, const CacheAttn& a, cudaStream_t s) {
+  static std::atomic<uint64_t> attr_devices{0};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (!(attr_devices.load() >> (dev & 63) & 1)) {
+    cudaFuncAttributes f;
+    cudaError_t e = cudaFuncGetAttributes(&f, Kernel);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kSmemMax - (int)f.sharedSizeBytes);
+    if (e != cudaSuccess) return e;
+    attr_devices |= 1ull << (dev & 63);
+  }
   smem = std::max(smem, sizeof(CacheSplitSpace));
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
-  if (e != cudaSuccess) return e;
-  return tc::launch_dependent(kernel, dim3(grid), dim3(threads), smem, s, 1, a);
+  return tc::launch_dependent(Kernel, dim3(grid), dim3(threads), smem, s, 1, a);
 }
 
 template <typename T>
@@ -685,18 +698,18 @@ cudaError_t attn_t(CacheAttn a, int num_sms, cudaStream_t s) {
                                           (size_t)warps * TP * r * 4);
     const size_t smem = TP * r * 4 + warps * TP * TK * 4 + tiles;
     a.never_cut = cache_most_tiles(a.c, TP, TK) <= 16;
-    if (r <= 32) e = launch_with(cache_tokens_kernel<T, 1>, num_sms, 32 * warps, smem, a, s);
-    else if (r <= 64) e = launch_with(cache_tokens_kernel<T, 2>, num_sms, 32 * warps, smem, a, s);
-    else if (r <= 128) e = launch_with(cache_tokens_kernel<T, 4>, num_sms, 32 * warps, smem, a, s);
-    else e = launch_with(cache_tokens_kernel<T, 8>, num_sms, 32 * warps, smem, a, s);
+    if (r <= 32) e = launch_with<cache_tokens_kernel<T, 1>>(num_sms, 32 * warps, smem, a, s);
+    else if (r <= 64) e = launch_with<cache_tokens_kernel<T, 2>>(num_sms, 32 * warps, smem, a, s);
+    else if (r <= 128) e = launch_with<cache_tokens_kernel<T, 4>>(num_sms, 32 * warps, smem, a, s);
+    else e = launch_with<cache_tokens_kernel<T, 8>>(num_sms, 32 * warps, smem, a, s);
   } else {
     mt = MT;
     const size_t smem = (MT + (r <= 128 ? 1 : 2) * KT) * pitch * sizeof(T) + MT * (KT + 4) * 4;
     a.never_cut = cache_most_tiles(a.c, MT, KT) <= 4;
     if (r <= 128) grid = 2 * num_sms;
-    if (r <= 64) e = launch_with(cache_rows_kernel<T, 1>, grid, 256, smem, a, s);
-    else if (r <= 128) e = launch_with(cache_rows_kernel<T, 2>, grid, 256, smem, a, s);
-    else e = launch_with(cache_rows_kernel<T, 4>, grid, 256, smem, a, s);
+    if (r <= 64) e = launch_with<cache_rows_kernel<T, 1>>(grid, 256, smem, a, s);
+    else if (r <= 128) e = launch_with<cache_rows_kernel<T, 2>>(grid, 256, smem, a, s);
+    else e = launch_with<cache_rows_kernel<T, 4>>(grid, 256, smem, a, s);
   }
   cache_launched(a, a.never_cut ? 1 : 2);
   if (e != cudaSuccess || a.never_cut) return e;
@@ -708,7 +721,7 @@ template <typename T>
 cudaError_t mass_t(const CacheAttn& a, int num_sms, cudaStream_t s) {
   const size_t smem = (MT + KT) * (a.c.r + 16 / sizeof(T)) * sizeof(T);
   const int grid = a.c.r <= 128 ? 2 * num_sms : num_sms;
-  cudaError_t e = launch_with(cache_mass_rows_kernel<T>, grid, 256, smem, a, s);
+  cudaError_t e = launch_with<cache_mass_rows_kernel<T>>(grid, 256, smem, a, s);
   if (e != cudaSuccess) return e;
   cache_launched(a, 2);
   return tc::launch_dependent(cache_mass_rows_join_kernel, dim3(grid), dim3(KT), 0, s, 1, a);

@@ -18,6 +18,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "cache.h"
 #include "cache_call.cuh"
@@ -677,10 +678,10 @@ cache_mass_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn
 template <int R>
 cudaError_t launch_mass_r(const CacheAttn& a, const CUtensorMap& tmC, int num_sms, cudaStream_t s) {
   using C = Cfg<R>;
-  static uint64_t attr_devices = 0;
+  static std::atomic<uint64_t> attr_devices{0};
   int dev = 0;
   cudaGetDevice(&dev);
-  if (!(attr_devices >> (dev & 63) & 1)) {
+  if (!(attr_devices.load() >> (dev & 63) & 1)) {
     cudaError_t e = cudaFuncSetAttribute(cache_mass_token_kernel<R>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
     if (e != cudaSuccess) return e;
@@ -694,10 +695,10 @@ cudaError_t launch_mass_r(const CacheAttn& a, const CUtensorMap& tmC, int num_sm
 template <int R>
 cudaError_t launch_r(CacheAttn a, const CUtensorMap& tmC, int num_sms, cudaStream_t s) {
   using C = Cfg<R>;
-  static uint64_t attr_devices = 0;
+  static std::atomic<uint64_t> attr_devices{0};
   int dev = 0;
   cudaGetDevice(&dev);
-  if (!(attr_devices >> (dev & 63) & 1)) {
+  if (!(attr_devices.load() >> (dev & 63) & 1)) {
     cudaError_t e = cudaFuncSetAttribute(cache_token_kernel<R>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
     if (e != cudaSuccess) return e;

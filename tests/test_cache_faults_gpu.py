@@ -1,11 +1,14 @@
-"""What callers of the paged cache get back for users that a call leaves out, and from
-repeated calls."""
+"""What callers of the paged cache get back for users that a call leaves out, from
+repeated calls, from calls on other streams and from several threads."""
+import threading
+
 import numpy as np
 import pytest
 import torch
 
 import oracle.cache as oc
 from cache_harness import DT, Case, attend_bounds, close, mass_bound
+from latent_attention_jagged_b200 import LatentCache
 from latent_attention_jagged_b200.binding import DEV_BAD_OFFSETS, DEV_TOO_LONG
 
 pytestmark = pytest.mark.gpu
@@ -88,3 +91,34 @@ def test_appending_again_clears_what_the_events_collected(dtype, rank):
         mass[pg[-m:], rw[-m:]] = 0.0
         bound[pg[-m:], rw[-m:]] = 0.0
     close(c.mass, mass, bound, "mass after the second append")
+
+
+def test_caches_of_other_ranks_in_several_threads():
+    # the same kernel with more and with less shared memory, from threads of their own
+    ranks = [100, 128, 100, 128, 68, 128]
+    cases = [Case("fp32", 2, r, 32, [60, 40], seed=70) for r in ranks]
+    calls, failed = [], []
+    for x in cases:
+        q, off = x.queries([1, 1], 0)
+        args = (q, torch.from_numpy(off).cuda(), x.dev("table"), x.dev("lengths"))
+        want = x.cache.attend(*args, scale=0.1).clone()
+        out = torch.empty_like(q)
+        stream = torch.cuda.Stream()
+        calls.append((x.cache, args, out, stream, want))
+    torch.cuda.synchronize()
+
+    def work(cache, args, out, stream, want):
+        try:
+            for _ in range(2000):
+                cache.attend(*args, scale=0.1, out=out, stream=stream)
+        except Exception as e:               # noqa: BLE001 - reported by the test
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=a) for a in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, failed
+    assert all(torch.equal(out, want) for _, _, out, _, want in calls)
