@@ -263,6 +263,13 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+def _int32(**numbers):
+    """Refuses what a C int32 field would cut off without an error."""
+    for name, n in numbers.items():
+        if not -0x80000000 <= n <= 0x7fffffff:
+            raise ValueError(f"{name} = {n} does not fit 32 bits")
+
+
 def _made(make, stream, device):
     """make(), a tensor for a call on `stream` (None: the current stream; else a torch
     stream or its address).  It comes from that stream's memory, whose earlier uses the
@@ -458,6 +465,7 @@ class Llatte:
         than min(keep) events is left out (see llatte_forward_cached)."""
         if getattr(self.dims, "d_time", 0):      # the code of an event changes with the request
             raise LlatteError(LLATTE_ERR_UNSUPPORTED, "llatte_forward_cached")
+        _int32(window=window, n_sink=n_sink)
         B = self._check_inputs(values, offsets, context, cand, None)
         n = len(self.dims.keep)
         if len(caches) != n:
@@ -671,6 +679,9 @@ class LatentCache:
         self.pool, self.mass, self.heads = pool, mass, int(heads)
         self.n_pages, self.page_size, self.rank = (int(n) for n in pool.shape)
         self.device, self.dt, self.index = pool.device, pool.dtype, pool.get_device()
+        _int32(heads=self.heads, max_batch=max_batch, max_pages=max_pages)
+        if not 0 <= max_rows < 1 << 63:
+            raise ValueError(f"max_rows = {max_rows}")
         c = llatte_cache_dims()
         c.heads, c.rank, c.page_size, c.n_pages = self.heads, self.rank, self.page_size, self.n_pages
         c.dtype = LLATTE_BF16 if self.dt == torch.bfloat16 else LLATTE_FP32
@@ -740,6 +751,7 @@ class LatentCache:
         `window` > 0 limits a row to that many events back from its position and
         the first n_sink.  `lse` (float32 [rows, heads]) receives the log of the
         softmax denominators; `accumulate` adds all weights to `mass`."""
+        _int32(n_cand=n_cand, window=window, n_sink=n_sink)
         v, B = self._view(table, lengths)
         if not self._fits(q, self.dt, 3) or q.shape[1:] != (self.heads, self.rank):
             self._refuse("q", self.dt, f"*, {self.heads}, {self.rank}")
@@ -771,6 +783,7 @@ class LatentCache:
         of dst_table (default: the user's own first pages).  Returns the new
         lengths; `kept` (int32 [B, budget]) receives the old slots.  A user left out
         (see the status) keeps what new_lengths held, by default the length given."""
+        _int32(budget=budget, n_sink=n_sink, n_recent=n_recent)
         v, B = self._view(table, lengths)
         if new_lengths is None:              # a user left out keeps its length
             new_lengths = _made(lambda: lengths.clone(), stream, self.device)

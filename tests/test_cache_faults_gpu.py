@@ -1,5 +1,5 @@
 """What callers of the paged cache get back for users that a call leaves out, from
-repeated calls, from calls on other streams and from several threads."""
+repeated calls and from several threads, and numbers that it cannot take."""
 import threading
 
 import numpy as np
@@ -122,3 +122,26 @@ def test_caches_of_other_ranks_in_several_threads():
     torch.cuda.synchronize()
     assert not failed, failed
     assert all(torch.equal(out, want) for _, _, out, _, want in calls)
+
+
+def test_numbers_that_do_not_fit_are_refused():
+    c = Case("bf16", 4, 128, 64, [70, 30], seed=6)
+    q, off = c.queries([1, 1], 1)
+    o, t, n = torch.from_numpy(off).cuda(), c.dev("table"), c.dev("lengths")
+    pool, mass = c.pool.clone(), c.mass.clone()
+    for k in (dict(n_cand=1 << 32), dict(window=(1 << 32) + 5), dict(n_sink=1 << 31),
+              dict(window=-(1 << 31) - 1)):
+        with pytest.raises(ValueError):
+            c.cache.attend(q, o, t, n, **k)
+    for k in (dict(budget=(1 << 32) + 4), dict(budget=8, n_sink=1 << 32),
+              dict(budget=8, n_recent=(1 << 32) + 1)):
+        with pytest.raises(ValueError):
+            c.cache.evict(t, n, **k)
+    for k in (dict(heads=(1 << 32) + 4), dict(max_batch=(1 << 32) + 2), dict(max_pages=1 << 32),
+              dict(max_rows=1 << 64)):
+        with pytest.raises(ValueError):
+            LatentCache(c.pool, **dict(dict(heads=4), **k))
+    torch.cuda.synchronize()
+    assert c.cache.status() == 0
+    assert torch.equal(torch.nan_to_num(c.pool), torch.nan_to_num(pool))
+    assert torch.equal(c.mass, mass)
