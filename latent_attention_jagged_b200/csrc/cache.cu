@@ -758,7 +758,8 @@ int llatte_cache_append(llatte_cache* h, const llatte_cache_view* v, const void*
                         const int64_t* offsets, const void* gain, float eps, void* stream) {
   const int rc = check_view(h, v);
   if (rc != LLATTE_OK) return rc;
-  if (rows < 0 || rows * (int64_t)h->dims.heads >= (int64_t)1 << 31) return LLATTE_ERR_ARG;
+  constexpr int64_t top = (int64_t)1 << 31;
+  if (rows < 0 || rows >= top || rows * h->dims.heads >= top) return LLATTE_ERR_ARG;
   if (v->B == 0 || rows == 0) return LLATTE_OK;
   if (!x || !offsets || (((uintptr_t)x | (uintptr_t)gain) & 15)) return LLATTE_ERR_ARG;
   if (gain && !(eps > 0.f)) return LLATTE_ERR_ARG;

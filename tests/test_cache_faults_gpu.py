@@ -1,5 +1,6 @@
 """What callers of the paged cache get back for users that a call leaves out, from
 repeated calls and from several threads, and numbers that it cannot take."""
+import ctypes
 import threading
 
 import numpy as np
@@ -9,7 +10,7 @@ import torch
 import oracle.cache as oc
 from cache_harness import DT, Case, attend_bounds, close, mass_bound
 from latent_attention_jagged_b200 import LatentCache
-from latent_attention_jagged_b200.binding import DEV_BAD_OFFSETS, DEV_TOO_LONG
+from latent_attention_jagged_b200.binding import DEV_BAD_OFFSETS, DEV_TOO_LONG, LLATTE_ERR_ARG
 
 pytestmark = pytest.mark.gpu
 
@@ -145,3 +146,14 @@ def test_numbers_that_do_not_fit_are_refused():
     assert c.cache.status() == 0
     assert torch.equal(torch.nan_to_num(c.pool), torch.nan_to_num(pool))
     assert torch.equal(c.mass, mass)
+
+
+def test_append_refuses_more_rows_than_it_can_count():
+    c = Case("bf16", 4, 64, 16, [20], seed=6)
+    x = torch.zeros(2, 64, dtype=torch.bfloat16, device="cuda")
+    off = torch.tensor([0, 2]).cuda()
+    v, _ = c.cache._view(c.dev("table"), c.dev("lengths"))
+    for rows in (-1, 1 << 29, 1 << 31, 1 << 61, 1 << 62, (1 << 63) - 1):
+        assert c.cache.lib.llatte_cache_append(
+            c.cache.h, ctypes.byref(v), x.data_ptr(), rows, off.data_ptr(), None, 1e-6,
+            None) == LLATTE_ERR_ARG
