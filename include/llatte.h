@@ -619,7 +619,9 @@ int llatte_cache_evict(llatte_cache* cache, const llatte_cache_view* view,
  *               (min(max_total or max_batch * max_len, max_batch * keep[0])
  *               + max_batch * n_q)
  *   views       host array [n_layers]; lengths count the new events.  Layers may
- *               name the same table and lengths: their pools are apart
+ *               name the same table where their pools are apart, and one pool (or
+ *               cache) where their tables name other pages; the same pool with
+ *               the same table is refused (LLATTE_ERR_ARG)
  *   window, n_sink, accumulate   as in llatte_cache_attn
  * LLATTE_ERR_UNSUPPORTED for a handle with a layer in MLA's per-head form (create it
  * with LLATTE_ATTN_ABSORBED), with d_time > 0 (the code of an event changes with the

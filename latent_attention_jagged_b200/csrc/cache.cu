@@ -663,6 +663,8 @@ int cache_layer_check(const llatte_cache* h, const llatte_cache_view* v, int hea
   return dev == h->device ? LLATTE_OK : LLATTE_ERR_ARG;
 }
 
+const void* cache_layer_pool(const llatte_cache* h) { return h->pool; }
+
 int cache_layer_run(llatte_cache* h, const llatte_cache_view* v, const CacheLayer& l,
                     int* launched, cudaStream_t s) {
   if (l.rows_h > 0) {

@@ -67,6 +67,7 @@ struct CacheLayer {
 };
 int cache_layer_check(const llatte_cache* h, const llatte_cache_view* v, int heads, int rank,
                       int dtype, int64_t rows_q, int accumulate, int keep);
+const void* cache_layer_pool(const llatte_cache* h);
 int cache_layer_run(llatte_cache* h, const llatte_cache_view* v, const CacheLayer& a,
                     int* launched, cudaStream_t s);
 

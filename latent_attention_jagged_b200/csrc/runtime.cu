@@ -1083,6 +1083,10 @@ int llatte_forward_cached(llatte_handle* h, const llatte_batch* b, const llatte_
     const int rc = cache_layer_check(fc->caches[l], v, D.heads, D.rank, D.dtype, h->max_rows_q,
                                      fc->accumulate, keep);
     if (rc != LLATTE_OK) return rc;
+    for (int k = 0; k < l; ++k)    // two layers may not write the same pages
+      if (v->B > 0 && v->table == fc->views[k].table &&
+          cache_layer_pool(fc->caches[l]) == cache_layer_pool(fc->caches[k]))
+        return LLATTE_ERR_ARG;
   }
   return forward_impl(h, b->values, b->offsets, b->B, b->context, b->cand, nullptr, out, stream, fc);
 }

@@ -9,8 +9,8 @@ import torch
 
 import oracle
 import oracle.cache as oc
-from latent_attention_jagged_b200 import LatentCache, LlatteError
-from latent_attention_jagged_b200.binding import (DEV_BAD_OFFSETS, DEV_TOO_LONG,
+from latent_attention_jagged_b200 import LatentCache, Llatte, LlatteError
+from latent_attention_jagged_b200.binding import (DEV_BAD_OFFSETS, DEV_TOO_LONG, LLATTE_ERR_ARG,
                                                   LLATTE_ERR_UNSUPPORTED)
 from oracle.model import rmsnorm, silu
 
@@ -132,6 +132,55 @@ def test_rows_of_a_user_left_out_hold_nothing_of_earlier_calls(dtype, kw, max_ne
         assert np.abs(got[u] - _without_attention(inp, u)).max() < tol
     ref = oracle.forward(inp)
     assert_close(got[[0, 3]], ref[[0, 3]], dtype, "users beside those left out")
+
+
+@pytest.mark.parametrize("dtype,kw", [
+    ("bf16", {}), ("bf16", dict(rank=128, heads=2, d_head=64)), ("fp32", dict(rank=32, n_q=1)),
+    ("bf16", dict(d=512, heads=8, d_head=64, rank=256, n_q=1))])
+def test_single_events_on_a_handle_for_single_events(dtype, kw):
+    # one new event and few query tokens a user: the attention's form for single tokens
+    inp = _inputs(dtype, **dict(dict(n_q=2), **kw))
+    big = Served(inp)
+    n = np.asarray(inp.lengths)
+    old = [int(x) for x in np.maximum(n - 1, 0)]
+    big.request([0] * len(n), old, accumulate=True)
+    h = Llatte(inp.dims, inp.layers, None, max_batch=len(n), max_len=1)
+    caches = [LatentCache(c.pool, inp.dims.heads, mass=c.mass, max_batch=len(n),
+                          max_rows=h.query_rows(), max_pages=big.table.shape[1])
+              for c in big.caches]
+    big.h, big.caches = h, caches
+    before = [c.mass.double().sum().item() for c in caches]
+    out = big.request(old, [int(x) for x in n], accumulate=True)
+    assert_close(out, oracle.forward(inp), dtype, f"single events {kw}")
+    rows = sum(inp.dims.n_q + 1 for x in n if x)
+    for c, b in zip(caches, before):             # every row that sees an event spends 1 a head
+        spent = c.mass.double().sum().item() - b
+        assert abs(spent - inp.dims.heads * rows) < 1e-3 * inp.dims.heads * rows
+
+
+def test_two_layers_may_not_write_the_same_pages():
+    inp = _inputs(lengths=[40, 7])
+    s = Served(inp, max_new=40)
+    one = s.caches
+    s.caches = [one[0], one[0]]
+    with pytest.raises(LlatteError) as e:
+        _call(s, [0, 0], [40, 7])
+    assert e.value.code == LLATTE_ERR_ARG
+    twin = LatentCache(one[0].pool, inp.dims.heads, max_batch=2, max_rows=s.h.query_rows(),
+                       max_pages=s.table.shape[1])
+    s.caches = [one[0], twin]                    # another cache over the same pool and table
+    with pytest.raises(LlatteError) as e:
+        _call(s, [0, 0], [40, 7])
+    assert e.value.code == LLATTE_ERR_ARG
+    # one cache for both layers, whose tables name other pages
+    both = torch.zeros(2 * one[0].n_pages, 32, 64, dtype=torch.bfloat16, device="cuda")
+    c = LatentCache(both, inp.dims.heads, max_batch=2, max_rows=s.h.query_rows(),
+                    max_pages=s.table.shape[1])
+    s.caches = [c, c]
+    out = _call(s, [0, 0], [40, 7], table=[s.table_d, s.table_d + one[0].n_pages])
+    torch.cuda.synchronize()
+    assert s.h.status() == 0 and c.status() == 0
+    assert_close(out.double().cpu().numpy(), oracle.forward(inp), "bf16", "one pool, two layers")
 
 
 def test_the_same_request_again():
