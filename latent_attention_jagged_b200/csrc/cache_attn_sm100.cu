@@ -306,8 +306,9 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         ++itm;
       }
       __syncwarp();
-      // after an abort the MMA thread may have left tiles unread
-      if (lane == 0 && *abort_flag) {
+      // Its last loads land before the producer goes, whoever reads them: a role that gives
+      // up later leaves them unread, and the CTA must not end before them.
+      if (lane == 0) {
         drain_ring(kv_full, KS, g, c.status);
         drain_ring(q_full, QBUF, qi, c.status);
       }

@@ -173,7 +173,7 @@ cache_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       ok = __shfl_sync(0xffffffffu, ok, 0);
     }
     __syncwarp();
-    if (lane == 0 && *abort_flag) {
+    if (lane == 0) {                       // (see cache_attn_sm100.cu)
       drain_ring(k_full, KS, kn, c.status);
       drain_ring(q_full, QS, qn, c.status);
     }

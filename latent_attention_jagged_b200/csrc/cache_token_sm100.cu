@@ -198,7 +198,7 @@ cache_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn p) {
       }
     }
     __syncwarp();
-    if (lane == 0 && *abort_flag) drain_ring(kv_full, KS, g, c.status);
+    if (lane == 0) drain_ring(kv_full, KS, g, c.status);   // (see cache_attn_sm100.cu)
     __syncwarp();
     }
   } else {
@@ -592,7 +592,7 @@ cache_mass_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn
       ++g;
     }
     __syncwarp();
-    if (lane == 0 && *abort_flag) drain_ring(kv_full, KS, g, c.status);
+    if (lane == 0) drain_ring(kv_full, KS, g, c.status);   // (see cache_attn_sm100.cu)
     __syncwarp();
   } else if (warp < NW) {
     const int grp = lane >> 2, t4 = lane & 3;          // event (and event + 8), pair column
