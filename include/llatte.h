@@ -647,6 +647,18 @@ int llatte_cache_get_status(llatte_cache* cache, int32_t* device_status);
 /* 1 when attention over the cache runs on the tensor cores, 0 on CUDA cores. */
 int llatte_cache_uses_tensor_cores(const llatte_cache* cache);
 
+/*
+ * Failure-detection aid, as llatte_inject_timeout is for a forward handle: with
+ * enable = 1 the attention and accumulation kernels of the calls that follow on this cache
+ * make a bounded wait run out (20 us) in every CTA that has work, with loads (and, in
+ * the forms for many rows, products) in flight.  The call sets LLATTE_DEV_TIMEOUT;
+ * its outputs, and the masses with accumulate = 1, are unspecified.  enable = 0 switches that
+ * off, and the next call computes the usual result.  Returns
+ * LLATTE_ERR_UNSUPPORTED for a cache on CUDA cores (whose kernels wait for nothing),
+ * LLATTE_ERR_ARG for another enable value.
+ */
+int llatte_cache_inject_timeout(llatte_cache* cache, int enable);
+
 /* Free the cache's workspace (synchronises its device); the pools stay the caller's. */
 void llatte_cache_destroy(llatte_cache* cache);
 

@@ -122,7 +122,7 @@ EXPORTS = ("llatte_create", "llatte_forward", "llatte_plan_export", "llatte_get_
            "llatte_tokenizer_destroy", "llatte_inject_timeout", "llatte_cache_workspace_bytes",
            "llatte_cache_create", "llatte_cache_append", "llatte_cache_attend",
            "llatte_cache_evict", "llatte_cache_get_status", "llatte_cache_uses_tensor_cores",
-           "llatte_cache_destroy", "llatte_forward_cached")
+           "llatte_cache_destroy", "llatte_forward_cached", "llatte_cache_inject_timeout")
 TOK_MAX_FIELDS = 8
 PLAN_STATIC_MAX_BATCH = 4096
 
@@ -200,6 +200,8 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.llatte_cache_get_status.restype = ctypes.c_int
     lib.llatte_cache_uses_tensor_cores.argtypes = [VP]
     lib.llatte_cache_uses_tensor_cores.restype = ctypes.c_int
+    lib.llatte_cache_inject_timeout.argtypes = [VP, ctypes.c_int]
+    lib.llatte_cache_inject_timeout.restype = ctypes.c_int
     lib.llatte_cache_destroy.argtypes = [VP]
     lib.llatte_cache_destroy.restype = None
     lib.llatte_forward_cached.argtypes = [VP, P(llatte_batch), P(llatte_forward_cache), VP, VP]
@@ -804,6 +806,14 @@ class LatentCache:
         if rc != LLATTE_OK:
             raise LlatteError(rc, "llatte_cache_evict")
         return new_lengths
+
+    def inject_timeout(self, enable: bool = True):
+        """Failure-detection aid: the attention calls that follow make a bounded wait run
+        out on purpose (status bit DEV_TIMEOUT, outputs and accumulated masses
+        unspecified) until switched off again."""
+        rc = self.lib.llatte_cache_inject_timeout(self.h, 1 if enable else 0)
+        if rc != LLATTE_OK:
+            raise LlatteError(rc, "llatte_cache_inject_timeout")
 
     def status(self) -> int:
         v = ctypes.c_int32(0)

@@ -26,6 +26,7 @@ struct llatte_cache {
   int32_t* list;         // [max_batch, max_pages * page_size] kept slots
   float* lse2;           // [max_rows, heads]
   bool tc;               // attention on the tensor cores
+  bool inject;           // the next calls' kernels make a wait run out
   CUtensorMap tmC;       // the pool, a page a box (tc)
   float* part_o;         // [2 num_sms, block rows, rank]
   float2* part_ml;       // [2 num_sms, block rows]
@@ -631,6 +632,7 @@ CacheAttn make_attn(const llatte_cache* h, const llatte_cache_view* v, const voi
   a.pool = h->pool; a.mass = h->mass; a.q = q; a.out = out;
   a.part_o = h->part_o; a.part_ml = h->part_ml; a.join = h->join;
   a.count = h->parts;
+  a.inject = h->inject;
   return a;
 }
 
@@ -836,6 +838,13 @@ int llatte_cache_get_status(llatte_cache* h, int32_t* device_status) {
 }
 
 int llatte_cache_uses_tensor_cores(const llatte_cache* h) { return h ? h->tc : LLATTE_ERR_ARG; }
+
+int llatte_cache_inject_timeout(llatte_cache* h, int enable) {
+  if (!h || (enable != 0 && enable != 1)) return LLATTE_ERR_ARG;
+  if (!h->tc) return LLATTE_ERR_UNSUPPORTED;
+  h->inject = enable != 0;
+  return LLATTE_OK;
+}
 
 void llatte_cache_destroy(llatte_cache* h) {
   if (!h) return;

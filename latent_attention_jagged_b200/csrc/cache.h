@@ -51,6 +51,7 @@ struct CacheAttn {
   int64_t pairs;             // (row, head) pairs of the call, as far as the host can tell
   int32_t min_quota;         // fewest tiles of a CTA's run
   bool never_cut;            // no block is cut between CTAs (then there is nothing to join)
+  bool inject;               // failure-detection test: every CTA makes one wait run out
   float scale2;              // scale * log2(e): scores in log2 units
 };
 

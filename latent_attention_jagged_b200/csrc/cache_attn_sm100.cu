@@ -421,6 +421,9 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
           mbar_arrive(&piece_full[st]);
         }
         __syncwarp();
+        // An injected timeout: with the first piece handed round, a wait for the end of the
+        // last product, which the pieces held back here keep from coming.
+        if (p.inject && !warp_wait(drain + 1, 0, abort_flag, c.status, kInjectTimeoutNs)) break;
       }
     }
   } else if (warp < 20) {

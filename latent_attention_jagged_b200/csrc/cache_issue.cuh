@@ -15,9 +15,12 @@ __device__ __forceinline__ bool elect_one() {
   return ok != 0;
 }
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity,
-                                          volatile int* abort_flag, int32_t* status) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
+                                          volatile int* abort_flag, int32_t* status,
+                                          uint64_t limit_ns = kWaitTimeoutNs) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status, limit_ns));
 }
+// Limit of the wait that an injected timeout makes run out.
+constexpr uint64_t kInjectTimeoutNs = 20000;
 
 // tma_load_2d whose lines are the first to leave L2 when they are read only once in a
 // call: they would push out everything else, the kernel's own code included.

@@ -210,6 +210,12 @@ cache_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
           if (last) umma_commit(&k_empty[ks]);
         }
         __syncwarp();
+        // an injected timeout: with a product and loads in flight, a wait for what this
+        // warp itself commits at its end
+        if (p.inject && !warp_wait(drain, 0, abort_flag, c.status, kInjectTimeoutNs)) {
+          ok = false;
+          break;
+        }
       }
       ++kn;
     }

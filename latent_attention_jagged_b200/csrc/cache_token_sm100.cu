@@ -131,7 +131,8 @@ cache_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn p) {
   uint64_t* kv_empty = kv_full + KS;       // [KS]
   volatile int* abort_flag = (volatile int*)(kv_empty + KS);
   volatile int* last_flag = abort_flag + 1;
-  CacheSplit* split = (CacheSplit*)(kv_empty + KS + 1);
+  uint64_t* never = kv_empty + KS + 1;     // nothing arrives (injected timeout)
+  CacheSplit* split = (CacheSplit*)(never + 1);
   static_assert((2 * KS + 2) * 8 + sizeof(CacheSplit) <= C::BAR_BYTES, "barriers");
   float* sm_m = (float*)((uint8_t*)bars + C::BAR_BYTES);   // [NW][MT]
   float* sm_l = sm_m + NW * MT;
@@ -142,6 +143,7 @@ cache_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn p) {
   const CacheCall& c = p.c;
   if (threadIdx.x == 0) {
     for (int s = 0; s < KS; ++s) { mbar_init(&kv_full[s], 1); mbar_init(&kv_empty[s], NW); }
+    mbar_init(never, 1);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmC);
@@ -209,7 +211,9 @@ cache_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn p) {
     // ------------------------------------------------------------ consumers
     const int grp = lane >> 2, t4 = lane & 3;          // row (and row + 8), column pair
     uint32_t g = 0;
-    bool ok = true;
+    // an injected timeout: this warp has given up before its first tile
+    bool ok = !(p.inject && warp == 0) ||
+              warp_wait(never, 0, abort_flag, c.status, kInjectTimeoutNs);
     // ldmatrix rows of this lane: events 8 * (lane / 16) + lane % 8 for S, and
     // 8 * (lane / 8 % 2) + lane % 8 for P C; 16-byte chunks are XORed with event % 8
     const uint32_t k_row = (warp * 16 + ((lane >> 4) << 3) + (lane & 7)) * 128;
@@ -539,13 +543,15 @@ cache_mass_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn
   uint64_t* kv_full = bars;                // [KS]
   uint64_t* kv_empty = kv_full + KS;       // [KS]
   volatile int* abort_flag = (volatile int*)(kv_empty + KS);
-  CacheSplit* split = (CacheSplit*)(kv_empty + KS + 1);
+  uint64_t* never = kv_empty + KS + 1;     // nothing arrives (injected timeout)
+  CacheSplit* split = (CacheSplit*)(never + 1);
 
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const CacheCall& c = p.c;
   if (threadIdx.x == 0) {
     for (int s = 0; s < KS; ++s) { mbar_init(&kv_full[s], 1); mbar_init(&kv_empty[s], NW); }
+    mbar_init(never, 1);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmC);
@@ -604,7 +610,9 @@ cache_mass_token_kernel(const __grid_constant__ CUtensorMap tmC, const CacheAttn
     uint32_t qb[R / 16][4];
     float lse[2][2];
     int32_t pos[2][2];
-    while (items.next(c, it)) {
+    const bool ok = !(p.inject && warp == 0) ||        // an injected timeout (see above)
+                    warp_wait(never, 0, abort_flag, c.status, kInjectTimeoutNs);
+    while (ok && items.next(c, it)) {
       const int st = g % KS;
       bool w = mbar_wait(&kv_full[st], (g / KS) & 1, abort_flag, c.status);
       if (!__all_sync(0xffffffffu, w)) break;
