@@ -548,7 +548,8 @@ int llatte_cache_append(llatte_cache* cache, const llatte_cache_view* view, cons
  *     out = sum_t softmax_t(scale * q . c_t) c_t,   lse = log sum_t exp(scale * q . c_t).
  * A row that sees nothing gives out = 0 and lse = -infinity.  What a row does
  * not see has no effect on it, whatever its bits; the result of a row that sees a
- * latent with an infinity or NaN is not specified (NaN where the softmax is).
+ * latent with an infinity or NaN is not specified (NaN where the softmax is), nor
+ * is what it adds to the masses of the events it sees.
  * Latents up to 2^70 in magnitude are in range.
  *   q, out       device [rows, heads, rank] in dtype, 16-byte aligned, apart; rows of
  *                `out` that belong to no user are left as they were
@@ -583,8 +584,10 @@ int llatte_cache_attend(llatte_cache* cache, const llatte_cache_view* view,
  * dst_table, or into the user's own first pages (dst_table == NULL), whose
  * other rows stay as they were.
  *   budget        >= 1;  n_sink + n_recent <= budget
- *   dst_table     device int32 [B, dst_stride] of pages that no other row of
- *                 either table names, or NULL
+ *   dst_table     device int32 [B, dst_stride] of pages that neither the view's
+ *                 table nor another row of dst_table names, or NULL.  A user's own
+ *                 pages in another table are not in place (rows would be
+ *                 overwritten before they are read): pass NULL for that
  *   new_lengths   device int32 [B], may be the view's lengths; the entries of users
  *                 left out stay as they were
  *   kept          device int32 [B, budget] or NULL: the old slots of the kept

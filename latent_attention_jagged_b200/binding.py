@@ -782,7 +782,8 @@ class LatentCache:
               stream=None) -> torch.Tensor:
         """Keep at most `budget` events per user: the first n_sink, the last n_recent
         and the heaviest of the others by `mass`, packed in order into the pages
-        of dst_table (default: the user's own first pages).  Returns the new
+        of dst_table, which `table` may not name (default: in place, into the user's
+        own first pages).  Returns the new
         lengths; `kept` (int32 [B, budget]) receives the old slots.  A user left out
         (see the status) keeps what new_lengths held, by default the length given."""
         _int32(budget=budget, n_sink=n_sink, n_recent=n_recent)
