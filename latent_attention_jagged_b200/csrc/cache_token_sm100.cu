@@ -11,8 +11,8 @@
 // 192 KB of tiles on their way.
 //
 // Measured (64 users, 2000 to 8000 events, 8 heads, rank 256: 159 MB): 45 us, half the
-// rate of HBM.  Its loads do not bound it (DRAM 37 % busy, tensor pipe 24 %, issue slots
-// 20 % in the kernel at 48 us): each of two warps a scheduler waits for its own chain of
+// rate of HBM.  Its loads do not bound it (DRAM 41 % busy, tensor pipe 25 %, issue slots
+// 17 %): each of two warps a scheduler waits for its own chain of
 // ldmatrix, products and softmax, 64 products a tile of which half are padding at 8
 // pairs.
 #include <cuda.h>
