@@ -279,11 +279,13 @@ def _made(make, stream, device):
     the call does not wait for.  The caller reads it on the current stream."""
     if stream is None:
         return make()
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream_ptr(stream).value or 0, device=device)
-    here = torch.cuda.current_stream(device)
-    if stream.cuda_stream == here.cuda_stream:
+    ptr, here = _stream_ptr(stream).value or 0, torch.cuda.current_stream(device)
+    if ptr == here.cuda_stream:
         return make()
+    if not isinstance(stream, torch.cuda.Stream):
+        # (ExternalStream takes 0 for "any stream")
+        stream = (torch.cuda.ExternalStream(ptr, device=device) if ptr
+                  else torch.cuda.default_stream(device))
     with torch.cuda.stream(stream):
         t = make()
     t.record_stream(here)
@@ -682,8 +684,8 @@ class LatentCache:
         self.n_pages, self.page_size, self.rank = (int(n) for n in pool.shape)
         self.device, self.dt, self.index = pool.device, pool.dtype, pool.get_device()
         _int32(heads=self.heads, max_batch=max_batch, max_pages=max_pages)
-        if not 0 <= max_rows < 1 << 63:
-            raise ValueError(f"max_rows = {max_rows}")
+        if not -1 << 63 <= max_rows < 1 << 63:
+            raise ValueError(f"max_rows = {max_rows} does not fit 64 bits")
         c = llatte_cache_dims()
         c.heads, c.rank, c.page_size, c.n_pages = self.heads, self.rank, self.page_size, self.n_pages
         c.dtype = LLATTE_BF16 if self.dt == torch.bfloat16 else LLATTE_FP32

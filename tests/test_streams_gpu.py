@@ -47,6 +47,24 @@ def test_a_stream_given_by_its_address():
                                              stream=None if s is None else s.cuda_stream))
 
 
+def test_the_default_stream_given_by_its_address():
+    # 0 is a stream like any other: the memory is the default stream's, not a third one's
+    c, args = _cache_call()
+    want = c.cache.attend(*args, scale=0.1).clone()
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(other):
+        _behind_a_write(lambda s: c.cache.attend(*args, scale=0.1, stream=None if s is None else 0))
+        out = c.cache.attend(*args, scale=0.1, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    held = out.data_ptr()
+    del out
+    torch.cuda.synchronize()
+    blocks = [torch.empty_like(want) for _ in range(64)]         # of the default stream
+    assert held in [b.data_ptr() for b in blocks]
+
+
 def test_eviction():
     c, args = _cache_call()
     _behind_a_write(lambda s: c.cache.evict(args[2], args[3], 5000, stream=s))
